@@ -947,6 +947,191 @@ moe_status moe_allreduce_rmsnorm_emulated(void* const* bufs, int32_t G, int32_t 
     return cuda_status(launch_allreduce_rmsnorm(a, ranks, true, st));
 }
 
+namespace {
+struct BalanceLayout {
+    size_t psum, cnt, info, term, arrived, total;
+};
+BalanceLayout balance_layout(int32_t T, int32_t E) {
+    BalanceLayout L{};
+    size_t off = kWsHeader;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += round_up(bytes, 256);
+        return at;
+    };
+    const size_t nb = (size_t)balance_blocks(T);
+    if (nb > 1) {  // one block finishes without partials
+        L.psum = take(nb * E * 4);
+        L.cnt = take(nb * E * 4);
+        L.info = take(nb * 8);
+        L.term = take((size_t)E * 8);
+        L.arrived = take(4);
+    }
+    L.total = off;
+    return L;
+}
+}  // namespace
+
+size_t moe_balance_workspace_bytes(int32_t T, int32_t E) {
+    if (T < 0 || E < 1 || E > 256) return 0;
+    return balance_layout(T, E).total;
+}
+
+moe_status moe_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int32_t T,
+                            int32_t E, int32_t k, float coef, float* loss, int32_t* counts,
+                            float* prob_mean, int32_t* tokens, void* ws, size_t ws_bytes,
+                            void* stream) {
+    if (T < 0 || E <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
+    if (E > 256 || k > 8 || k > E || (int64_t)T * k >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+    if (loss == nullptr || counts == nullptr || prob_mean == nullptr || tokens == nullptr)
+        return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (logits == nullptr || ids == nullptr || !aligned16(logits)))
+        return MOE_ERR_INVALID_ARG;
+    const BalanceLayout L = balance_layout(T, E);
+    const moe_status r = check_ws(ws, ws_bytes, L.total);
+    if (r != MOE_OK) return r;
+    if (!device_ok()) return MOE_ERR_UNSUPPORTED;
+    const BalancePartials part{at<float>(ws, L.psum), at<int32_t>(ws, L.cnt), at<int32_t>(ws, L.info),
+                               at<double>(ws, L.term), at<int32_t>(ws, L.arrived)};
+    const BalanceOut out{loss, counts, prob_mean, tokens, at<int32_t>(ws, 0), coef};
+    return cuda_status(
+        launch_balance_loss(logits, ids, mask, T, E, k, part, out, as_stream(stream)));
+}
+
+moe_status moe_route_backward(const float* logits, const int32_t* ids, const float* w,
+                              const float* dw, const uint8_t* mask, int32_t T, int32_t E, int32_t k,
+                              int32_t renormalize, const float* dloss, float coef,
+                              const int32_t* counts, const int32_t* tokens, float* dlogits,
+                              void* stream) {
+    if (T < 0 || E <= 0 || k <= 0) return MOE_ERR_INVALID_ARG;
+    if (E > 256 || k > 8 || k > E || (int64_t)T * k >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if ((dw == nullptr && dloss == nullptr) || (dw != nullptr && (ids == nullptr || w == nullptr)) ||
+        (dloss != nullptr && (counts == nullptr || tokens == nullptr)))
+        return MOE_ERR_INVALID_ARG;
+    if (logits == nullptr || dlogits == nullptr || !aligned16(logits) || !aligned16(dlogits))
+        return MOE_ERR_INVALID_ARG;
+    if (!device_ok()) return MOE_ERR_UNSUPPORTED;
+    const RouteBackwardArgs a{logits, ids, w, dw, mask, dloss, counts, tokens,
+                              dlogits, T, E, k, renormalize != 0 ? 1 : 0, coef};
+    return cuda_status(launch_route_backward(a, as_stream(stream)));
+}
+
+namespace {
+// Shape and group limits shared by the FP8 block products.
+moe_status check_product(const int32_t* offsets, int32_t G, int32_t M, int32_t N, int32_t K) {
+    if (G <= 0 || M < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID_ARG;
+    if (offsets == nullptr && G != 1) return MOE_ERR_INVALID_ARG;
+    if (N % 128 != 0 || K % 128 != 0 || G > 256 || (int64_t)G * N >= ((int64_t)1 << 31) ||
+        (int64_t)G * K >= ((int64_t)1 << 31))
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+moe_status run_product(bool forward, const uint8_t* a, const float* a_scale, const uint8_t* w,
+                       const float* w_scale, const int32_t* offsets, int32_t G, int32_t M, int32_t N,
+                       int32_t K, void* out, int32_t out_type, void* ws, size_t ws_bytes,
+                       void* stream) {
+    moe_status r = check_product(offsets, G, M, N, K);
+    if (r != MOE_OK) return r;
+    if (out_type != MOE_OUT_BF16 && out_type != MOE_OUT_F16 && out_type != MOE_OUT_F32)
+        return MOE_ERR_UNSUPPORTED;
+    if (M == 0) return MOE_OK;
+    if (a == nullptr || a_scale == nullptr || w == nullptr || w_scale == nullptr || out == nullptr ||
+        !aligned16(a) || !aligned16(w) || !aligned16(out))
+        return MOE_ERR_INVALID_ARG;
+    if ((r = check_ws(ws, ws_bytes, kWsHeader)) != MOE_OK) return r;
+    if (!device_ok()) return MOE_ERR_UNSUPPORTED;
+    Fp8ProductArgs p{};
+    p.a = a;
+    p.a_scale = a_scale;
+    p.b = w;
+    p.b_scale = w_scale;
+    p.offsets = offsets;
+    p.G = G;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.out = out;
+    p.out_type = out_type;
+    p.status = at<int32_t>(ws, 0);
+    p.timeout_ns = kDefaultTimeoutNs;
+    if (cudaMemsetAsync(p.status, 0, sizeof(int32_t), as_stream(stream)) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return cuda_status((forward ? launch_gemm_fp8 : launch_gemm_fp8_dgrad)(p, as_stream(stream)));
+}
+}  // namespace
+
+moe_status moe_gemm_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w,
+                        const float* w_scale, const int32_t* offsets, int32_t G, int32_t M,
+                        int32_t N, int32_t K, void* y, int32_t out_type, void* ws, size_t ws_bytes,
+                        void* stream) {
+    return run_product(true, x, x_scale, w, w_scale, offsets, G, M, N, K, y, out_type, ws, ws_bytes,
+                       stream);
+}
+
+moe_status moe_gemm_fp8_dgrad(const uint8_t* dy, const float* dy_scale, const uint8_t* w,
+                              const float* w_scale, const int32_t* offsets, int32_t G, int32_t M,
+                              int32_t N, int32_t K, void* dx, int32_t out_type, void* ws,
+                              size_t ws_bytes, void* stream) {
+    return run_product(false, dy, dy_scale, w, w_scale, offsets, G, M, N, K, dx, out_type, ws,
+                       ws_bytes, stream);
+}
+
+int64_t moe_fp8_token_rows(int32_t M, int32_t G) {
+    return M < 0 || G <= 0 ? 0 : fp8_token_rows(M, G);
+}
+
+moe_status moe_quantize_fp8_tokens(const uint16_t* x, const int32_t* offsets, int32_t G, int32_t M,
+                                   int32_t cols, uint8_t* q_t, float* scale_t, void* stream) {
+    const moe_status r = check_product(offsets, G, M, cols, 128);
+    if (r != MOE_OK) return r;
+    if (M == 0) return MOE_OK;
+    if (x == nullptr || q_t == nullptr || scale_t == nullptr || !aligned16(x) || !aligned16(q_t))
+        return MOE_ERR_INVALID_ARG;
+    if (fp8_token_rows(M, G) / 128 > 65535) return MOE_ERR_UNSUPPORTED;
+    if (!device_ok()) return MOE_ERR_UNSUPPORTED;
+    return cuda_status(launch_quant_tokens(x, offsets, G, M, cols, q_t, scale_t, as_stream(stream)));
+}
+
+moe_status moe_gemm_fp8_wgrad(const uint8_t* dy_t, const float* dy_t_scale, const uint8_t* x_t,
+                              const float* x_t_scale, const int32_t* offsets, int32_t G, int32_t M,
+                              int32_t N, int32_t K, float* dw, int32_t accumulate, void* ws,
+                              size_t ws_bytes, void* stream) {
+    moe_status r = check_product(offsets, G, M, N, K);
+    if (r != MOE_OK) return r;
+    if (dw == nullptr || !aligned16(dw)) return MOE_ERR_INVALID_ARG;
+    if (M > 0 && (dy_t == nullptr || dy_t_scale == nullptr || x_t == nullptr || x_t_scale == nullptr ||
+                  !aligned16(dy_t) || !aligned16(x_t)))
+        return MOE_ERR_INVALID_ARG;
+    if ((r = check_ws(ws, ws_bytes, kWsHeader)) != MOE_OK) return r;
+    if (fp8_token_rows(M, G) / 128 > 65535) return MOE_ERR_UNSUPPORTED;
+    if (!device_ok()) return MOE_ERR_UNSUPPORTED;
+    if (M == 0) {  // the operands are empty: nothing to add, or zeros
+        if (accumulate) return MOE_OK;
+        return cuda_status(cudaMemsetAsync(dw, 0, (size_t)G * N * K * 4, as_stream(stream)));
+    }
+    Fp8ProductArgs p{};
+    p.a = dy_t;
+    p.a_scale = dy_t_scale;
+    p.b = x_t;
+    p.b_scale = x_t_scale;
+    p.offsets = offsets;
+    p.G = G;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.rows_t = fp8_token_rows(M, G);
+    p.out = dw;
+    p.out_type = MOE_OUT_F32;
+    p.accumulate = accumulate != 0 ? 1 : 0;
+    p.status = at<int32_t>(ws, 0);
+    p.timeout_ns = kDefaultTimeoutNs;
+    if (cudaMemsetAsync(p.status, 0, sizeof(int32_t), as_stream(stream)) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return cuda_status(launch_gemm_fp8_wgrad(p, as_stream(stream)));
+}
+
 moe_status moe_read_device_status(const void* ws, void* stream) {
     if (ws == nullptr) return MOE_ERR_INVALID_ARG;
     cudaStream_t st = as_stream(stream);

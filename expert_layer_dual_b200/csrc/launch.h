@@ -226,6 +226,69 @@ cudaError_t launch_lamport_init(void* buf, size_t bytes, cudaStream_t s);
 cudaError_t launch_allreduce_rmsnorm(const ArNormArgs& a, int ranks_in_launch, bool cooperative,
                                      cudaStream_t s);
 
+// ---- gemm_fp8_block.cu (FP8 block-128 product, its gradients, token-block quantiser)
+// Rows of the token-block layout: every group's rows padded to 128 (at most
+// min(G, M) groups hold a row, each with at most 127 rows of padding).
+inline int64_t fp8_token_rows(int64_t M, int64_t G) {
+    return (M + 127 * (G < M ? G : M)) / 128 * 128;
+}
+struct Fp8ProductArgs {
+    const uint8_t* a;        // x, dy, or dy_t
+    const float* a_scale;
+    const uint8_t* b;        // w, w, or x_t
+    const float* b_scale;
+    const int32_t* offsets;  // [G+1] or nullptr (one group of all rows)
+    int G, M, N, K;
+    int64_t rows_t;          // wgrad: columns of the transposed operands
+    void* out;
+    int out_type;            // MOE_OUT_*
+    int accumulate;          // wgrad: add to out
+    int32_t* status;
+    uint64_t timeout_ns;
+};
+cudaError_t launch_gemm_fp8(const Fp8ProductArgs& a, cudaStream_t s);
+cudaError_t launch_gemm_fp8_dgrad(const Fp8ProductArgs& a, cudaStream_t s);
+cudaError_t launch_gemm_fp8_wgrad(const Fp8ProductArgs& a, cudaStream_t s);
+cudaError_t launch_quant_tokens(const uint16_t* x, const int32_t* offsets, int G, int M, int cols,
+                                uint8_t* q, float* scale, cudaStream_t s);
+
+// ---- balance.cu (load-balance loss, per-expert counts, gradient of the router logits)
+constexpr int kBalanceOneBlock = 512;   // up to this many tokens one block does it all
+constexpr int kBalanceMaxBlocks = 592;  // blocks of the first pass (four per SM)
+struct BalancePartials {                // workspace of the two-pass form
+    float* psum;       // [blocks][E]
+    int32_t* cnt;      // [blocks][E]
+    int32_t* info;     // [blocks][2]: tokens that count, an id out of range seen
+    double* term;      // [E]
+    int32_t* arrived;
+};
+struct BalanceOut {
+    float* loss;
+    int32_t* counts;
+    float* prob_mean;
+    int32_t* tokens;
+    int32_t* status;
+    float coef;
+};
+int balance_blocks(int T);
+cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int T,
+                                int E, int k, const BalancePartials& part, const BalanceOut& out,
+                                cudaStream_t s);
+struct RouteBackwardArgs {
+    const float* logits;
+    const int32_t* ids;
+    const float* w;
+    const float* dw;        // or nullptr
+    const uint8_t* mask;    // or nullptr
+    const float* dloss;     // or nullptr
+    const int32_t* counts;
+    const int32_t* tokens;
+    float* dlogits;
+    int T, E, k, renorm;
+    float coef;
+};
+cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s);
+
 // ---- tensor maps (api.cu)
 // 2-D row-major tensor [rows][cols] of `elem_bytes`-sized elements, box
 // [box_rows][box_cols], 128-byte swizzle, zero fill out of bounds.

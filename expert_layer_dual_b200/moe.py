@@ -43,7 +43,11 @@ EXPORTS = ["moe_status_string", "moe_workspace_bytes", "moe_permute_workspace_by
            "moe_calibrate_fp8_static", "moe_route", "moe_ep_dispatch", "moe_gather_rows",
            "moe_lamport_buffer_bytes", "moe_lamport_init", "moe_allreduce_rmsnorm",
            "moe_allreduce_rmsnorm_emulated", "moe_peer_buffer_alloc", "moe_peer_buffer_open",
-           "moe_peer_buffer_close", "moe_peer_buffer_free"]
+           "moe_peer_buffer_close", "moe_peer_buffer_free",
+           "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_backward",
+           "moe_gemm_fp8", "moe_gemm_fp8_dgrad", "moe_fp8_token_rows", "moe_quantize_fp8_tokens",
+           "moe_gemm_fp8_wgrad"]
+OUT_BF16, OUT_F16, OUT_F32 = range(3)
 
 
 class moe_shape(ctypes.Structure):
@@ -111,6 +115,18 @@ _sig = {
     "moe_peer_buffer_open": (_i32, [_vp, ctypes.POINTER(_vp)]),
     "moe_peer_buffer_close": (_i32, [_vp]),
     "moe_peer_buffer_free": (_i32, [_vp]),
+    "moe_balance_workspace_bytes": (_sz, [_i32, _i32]),
+    "moe_balance_loss": (_i32, [_vp, _vp, _vp, _i32, _i32, _i32, ctypes.c_float, _vp, _vp, _vp, _vp,
+                                _vp, _sz, _vp]),
+    "moe_route_backward": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp,
+                                  ctypes.c_float, _vp, _vp, _vp, _vp]),
+    "moe_gemm_fp8": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _sz, _vp]),
+    "moe_gemm_fp8_dgrad": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _sz,
+                                  _vp]),
+    "moe_fp8_token_rows": (_i64, [_i32, _i32]),
+    "moe_quantize_fp8_tokens": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]),
+    "moe_gemm_fp8_wgrad": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _sz,
+                                  _vp]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -402,6 +418,159 @@ def combine(shape, o, inv, w, y, stream=None):
 def forward(shape, weights, x, y, ws, stream=None):
     _check(_lib.moe_forward(ctypes.byref(shape), ctypes.byref(weights), _p(x), _p(y), _p(ws),
                             ws.numel() * ws.element_size(), _stream(stream)), "moe_forward")
+
+
+# ------------------------------------------------------------------ training entry points
+_OUT_TYPES = {torch.bfloat16: OUT_BF16, torch.uint16: OUT_BF16, torch.float16: OUT_F16,
+              torch.float32: OUT_F32}
+
+
+def _want(name, t, shape, dtypes, like=None):
+    """Refuses a tensor whose shape, type or device is not the call's."""
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: type {t.dtype} is not accepted")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {like.device}")
+
+
+def _launch_device(t):
+    """The library launches on the current device: its tensors have to be there."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {t.device}, not on the current CUDA device")
+
+
+_F32, _I32 = (torch.float32,), (torch.int32,)
+_CODES = (torch.uint8, torch.float8_e4m3fn)
+_MASK = (torch.uint8, torch.bool)
+
+
+def balance_workspace_bytes(T: int, E: int) -> int:
+    return int(_lib.moe_balance_workspace_bytes(T, E))
+
+
+def balance_loss(logits, ids, mask, coef, loss, counts, prob_mean, tokens, ws, stream=None):
+    """moe_balance_loss: loss [1], counts [E], prob_mean [E] and tokens [1] of
+    logits [T, E] and the selected ids [T, k]; mask [T] (uint8 or bool) or None."""
+    T, E = logits.shape
+    k = ids.shape[1]
+    _launch_device(logits)
+    _want("logits", logits, (T, E), _F32)
+    _want("ids", ids, (T, k), _I32, logits)
+    if mask is not None:
+        _want("mask", mask, (T,), _MASK, logits)
+    _want("loss", loss, (1,), _F32, logits)
+    _want("counts", counts, (E,), _I32, logits)
+    _want("prob_mean", prob_mean, (E,), _F32, logits)
+    _want("tokens", tokens, (1,), _I32, logits)
+    _check(_lib.moe_balance_loss(_p(logits), _p(ids), _p(mask), T, E, k, float(coef), _p(loss),
+                                 _p(counts), _p(prob_mean), _p(tokens), _p(ws),
+                                 ws.numel() * ws.element_size(), _stream(stream)), "moe_balance_loss")
+
+
+def route_backward(logits, ids, w, dw, mask, renormalize, dloss, coef, counts, tokens, dlogits,
+                   stream=None):
+    """moe_route_backward: dlogits [T, E] from the gradient dw [T, k] of the
+    top-k weights w (None: without that part) and dloss [1] of the balance loss
+    (None: without it); w may be None without dw, counts and tokens without
+    dloss."""
+    T, E = logits.shape
+    k = ids.shape[1]
+    _launch_device(logits)
+    _want("logits", logits, (T, E), _F32)
+    _want("ids", ids, (T, k), _I32, logits)
+    if dw is not None:
+        _want("dw", dw, (T, k), _F32, logits)
+        _want("w", w, (T, k), _F32, logits)
+    if mask is not None:
+        _want("mask", mask, (T,), _MASK, logits)
+    if dloss is not None:
+        _want("dloss", dloss, (1,), _F32, logits)
+        _want("counts", counts, (E,), _I32, logits)
+        _want("tokens", tokens, (1,), _I32, logits)
+    _want("dlogits", dlogits, (T, E), _F32, logits)
+    _check(_lib.moe_route_backward(_p(logits), _p(ids), _p(w), _p(dw), _p(mask), T, E, k,
+                                   int(bool(renormalize)), _p(dloss), float(coef), _p(counts),
+                                   _p(tokens), _p(dlogits), _stream(stream)), "moe_route_backward")
+
+
+def _weight_shape(w_q, offsets):
+    """(G, N, K) of weight codes [N, K] or [G, N, K]."""
+    G, (N, K) = (w_q.shape[0] if w_q.dim() == 3 else 1), w_q.shape[-2:]
+    if offsets is None and G != 1:
+        raise ValueError("several weight matrices need offsets")
+    return G, N, K
+
+
+def _product(entry, name, a_q, a_s, w_q, w_s, offsets, out, a_cols, out_cols, G, N, K, ws, stream):
+    M = a_q.shape[0]
+    _launch_device(a_q)
+    _want("codes", a_q, (M, a_cols), _CODES)
+    _want("scales", a_s, (M, a_cols // 128), _F32, a_q)
+    _want("weight codes", w_q, w_q.shape, _CODES, a_q)
+    _want("weight scales", w_s, tuple(w_q.shape[:-2]) + (N // 128, K // 128), _F32, a_q)
+    if offsets is not None:
+        _want("offsets", offsets, (G + 1,), _I32, a_q)
+    _want("output", out, (M, out_cols), _OUT_TYPES, a_q)
+    _check(entry(_p(a_q), _p(a_s), _p(w_q), _p(w_s), _p(offsets), G, M, N, K, _p(out),
+                 _OUT_TYPES[out.dtype], _p(ws), ws.numel() * ws.element_size(), _stream(stream)), name)
+
+
+def gemm_fp8(x_q, x_s, w_q, w_s, offsets, y, ws, stream=None):
+    """moe_gemm_fp8: y [M, N] (bf16, f16 or f32) = x W^T from e4m3 codes x_q
+    [M, K], w_q [N, K] or [G, N, K] and their 1x128 / 128x128 scales; offsets
+    [G+1] (int32) or None for one matrix."""
+    G, N, K = _weight_shape(w_q, offsets)
+    _product(_lib.moe_gemm_fp8, "moe_gemm_fp8", x_q, x_s, w_q, w_s, offsets, y, K, N, G, N, K, ws,
+             stream)
+
+
+def gemm_fp8_dgrad(dy_q, dy_s, w_q, w_s, offsets, dx, ws, stream=None):
+    """moe_gemm_fp8_dgrad: dx [M, K] = dy W from dy's codes [M, N] and the
+    forward's weight codes and scales."""
+    G, N, K = _weight_shape(w_q, offsets)
+    _product(_lib.moe_gemm_fp8_dgrad, "moe_gemm_fp8_dgrad", dy_q, dy_s, w_q, w_s, offsets, dx, N, K, G,
+             N, K, ws, stream)
+
+
+def fp8_token_rows(M: int, G: int = 1) -> int:
+    return int(_lib.moe_fp8_token_rows(M, G))
+
+
+def quantize_fp8_tokens(x, offsets, q_t, scale_t, stream=None):
+    """moe_quantize_fp8_tokens: x [M, cols] (bf16) -> q_t [cols, R] e4m3 codes,
+    scale_t [R/128, cols], R = fp8_token_rows(M, G)."""
+    M, cols = x.shape
+    G = 1 if offsets is None else offsets.numel() - 1
+    R = fp8_token_rows(M, G)
+    _launch_device(x)
+    _want("x", x, (M, cols), (torch.bfloat16, torch.uint16))
+    if offsets is not None:
+        _want("offsets", offsets, (G + 1,), _I32, x)
+    _want("codes", q_t, (cols, R), _CODES, x)
+    _want("scales", scale_t, (R // 128, cols), _F32, x)
+    _check(_lib.moe_quantize_fp8_tokens(_p(x), _p(offsets), G, M, cols, _p(q_t), _p(scale_t),
+                                        _stream(stream)), "moe_quantize_fp8_tokens")
+
+
+def gemm_fp8_wgrad(dy_t, dy_ts, x_t, x_ts, offsets, M, dw, accumulate, ws, stream=None):
+    """moe_gemm_fp8_wgrad: dw [N, K] or [G, N, K] (f32) = (or +=, accumulate)
+    dy^T x over each group's rows, from quantize_fp8_tokens' outputs."""
+    G, N, K = _weight_shape(dw, offsets)
+    R = fp8_token_rows(M, G)
+    _launch_device(dw)
+    _want("dw", dw, dw.shape, _F32)
+    _want("dy codes", dy_t, (N, R), _CODES, dw)
+    _want("dy scales", dy_ts, (R // 128, N), _F32, dw)
+    _want("x codes", x_t, (K, R), _CODES, dw)
+    _want("x scales", x_ts, (R // 128, K), _F32, dw)
+    if offsets is not None:
+        _want("offsets", offsets, (G + 1,), _I32, dw)
+    _check(_lib.moe_gemm_fp8_wgrad(_p(dy_t), _p(dy_ts), _p(x_t), _p(x_ts), _p(offsets), G, M, N, K,
+                                   _p(dw), int(bool(accumulate)), _p(ws),
+                                   ws.numel() * ws.element_size(), _stream(stream)),
+           "moe_gemm_fp8_wgrad")
 
 
 PROFILE_EVENTS = 8

@@ -79,6 +79,11 @@ typedef int32_t moe_status;
                                        scale per matrix; activations e4m3 with
                                        static (calibrated) scales act_scale_x/h    */
 
+/* Output types of moe_gemm_fp8 and moe_gemm_fp8_dgrad. */
+#define MOE_OUT_BF16 0              /* one rounding to nearest even                */
+#define MOE_OUT_F16 1               /* the same, saturating at +-65504             */
+#define MOE_OUT_F32 2
+
 /* Layer shape.  T tokens of hidden size d; E routed experts of intermediate
  * size I, top-k routing; I_shared = 0 (no shared expert) or I. */
 typedef struct moe_shape {
@@ -462,6 +467,107 @@ moe_status moe_peer_buffer_alloc(size_t bytes, void** ptr, void* ipc_handle);
 moe_status moe_peer_buffer_open(const void* ipc_handle, void** ptr);
 moe_status moe_peer_buffer_close(void* ptr);
 moe_status moe_peer_buffer_free(void* ptr);
+
+/* ---------------------------------------------------------------- training
+ * The router's and the FP8 products' training side (no counterpart on the
+ * pages, which describe the forward only).  They follow the conventions above.
+ */
+
+/* Workspace bytes of moe_balance_loss (0 on a negative T or E out of 1..256). */
+size_t moe_balance_workspace_bytes(int32_t T, int32_t E);
+
+/* Load-balance loss of a router and its per-expert counts.  For logits [T][E]
+ * f32, the selected ids [T][k] (moe_route_topk's) and mask [T] (uint8, a token
+ * counts where it is not 0; NULL: every token counts), with P[t] = softmax of
+ * logits[t] over all E and n the number of tokens that count:
+ *   counts[e]    = assignments of those tokens to expert e     (int32 [E])
+ *   prob_mean[e] = (1/n) sum_t P[t][e]                          (f32 [E])
+ *   tokens[0]    = n                                            (int32)
+ *   loss[0]      = coef * sum_e (E counts[e] / (k n)) prob_mean[e]
+ * (coef when every expert is used alike).  n == 0 (T == 0 among it) gives
+ * zeros.  Tokens that do not count are not read: their logits may hold NaN.
+ * -inf logits have probability 0; a row that holds nothing else gives zeros.
+ * An id outside [0, E) of a token that counts is not counted and sets
+ * MOE_ERR_DEVICE_BAD_INDEX in ws's status word.  Deterministic.
+ * 1 <= E <= 256, 1 <= k <= min(E, 8); logits 16-byte aligned.
+ * ws: moe_balance_workspace_bytes(T, E) bytes. */
+moe_status moe_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int32_t T,
+                            int32_t E, int32_t k, float coef, float* loss, int32_t* counts,
+                            float* prob_mean, int32_t* tokens, void* ws, size_t ws_bytes,
+                            void* stream);
+
+/* Gradient of the router logits, dlogits [T][E] f32 (written whole), the sum of
+ *  - dw != NULL: the top-k weights' part for the upstream gradient dw [T][k] of
+ *    w [T][k] (moe_route_topk's output for ids and renormalize):
+ *      renormalize 1: dlogits[t][ids[t][j]] += w_j (dw_j - sum_i w_i dw_i)
+ *      renormalize 0: P[t][e] (sum_{j: ids[t][j] = e} dw_j - sum_i w_i dw_i)
+ *  - dloss != NULL: moe_balance_loss's part for its upstream gradient dloss[0]
+ *    and the same coef; counts, tokens as that call wrote them (or summed over
+ *    the ranks of a data-parallel group, for the loss of the whole batch):
+ *      dloss coef / n * P[t][e] (f_e - sum_j f_j P[t][j]), f_e = E counts[e] / (k n)
+ * At least one of the two.  Tokens with mask 0 get zeros and are not read; n ==
+ * 0 makes the loss's part zero.  ids outside [0, E) receive nothing.  ids and w
+ * are read only with dw, counts and tokens only with dloss (else they may be
+ * NULL).  logits and dlogits 16-byte aligned; dlogits may be logits itself. */
+moe_status moe_route_backward(const float* logits, const int32_t* ids, const float* w,
+                              const float* dw, const uint8_t* mask, int32_t T, int32_t E, int32_t k,
+                              int32_t renormalize, const float* dloss, float coef,
+                              const int32_t* counts, const int32_t* tokens, float* dlogits,
+                              void* stream);
+
+/* FP8 e4m3 matrix product with one FP32 scale per block of 128, y = x W^T:
+ *   y[m][n] = sum_b x_scale[m][b] w_scale[g][n/128][b]
+ *                   * sum_{k = 128b}^{128b+127} x[m][k] w[g][n][k]
+ * x [M][K] with x_scale [M][K/128] (moe_quantize_act_fp8), w [G][N][K] with
+ * w_scale [G][N/128][K/128] (moe_quantize_weights_fp8).  FP32 accumulation.
+ * offsets == NULL: G == 1, one matrix for all rows.  Else int32 [G+1] on the
+ * device (as moe_permute writes them): rows offsets[g] .. offsets[g+1]-1 use
+ * matrix g; rows before offsets[0] and from offsets[G] on are left as they are,
+ * and so is the output of a group without rows.  (Offsets out of order or out of
+ * range are clamped: no row outside the matrices is touched.)
+ * y [M][N] of type out_type (MOE_OUT_*).  N % 128 == 0, K % 128 == 0, M >= 0,
+ * 1 <= G <= 256, G*N and G*K < 2^31.  x, w, y 16-byte aligned.  ws: 256 bytes. */
+moe_status moe_gemm_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w,
+                        const float* w_scale, const int32_t* offsets, int32_t G, int32_t M,
+                        int32_t N, int32_t K, void* y, int32_t out_type, void* ws, size_t ws_bytes,
+                        void* stream);
+
+/* Input gradient of moe_gemm_fp8, dx = dy W, with the same weight codes and
+ * scales (no transposed copy):
+ *   dx[m][k] = sum_b dy_scale[m][b] w_scale[g][b][k/128]
+ *                    * sum_{n = 128b}^{128b+127} dy[m][n] w[g][n][k]
+ * dy [M][N] with dy_scale [M][N/128] (moe_quantize_act_fp8); dx [M][K].  Groups,
+ * types and limits as moe_gemm_fp8. */
+moe_status moe_gemm_fp8_dgrad(const uint8_t* dy, const float* dy_scale, const uint8_t* w,
+                              const float* w_scale, const int32_t* offsets, int32_t G, int32_t M,
+                              int32_t N, int32_t K, void* dx, int32_t out_type, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* Columns of the token-block layout below for M rows in G groups (a multiple of
+ * 128; 0 for M == 0 or a bad argument). */
+int64_t moe_fp8_token_rows(int32_t M, int32_t G);
+
+/* Quantisation along the tokens, transposed, of the weight gradient's operands:
+ * x [M][cols] bf16 (cols % 128 == 0) -> q_t [cols][R] e4m3, scale_t [R/128][cols],
+ * R = moe_fp8_token_rows(M, G).  The rows of the groups (offsets, G as for
+ * moe_gemm_fp8) follow one another, each group's padded with zero codes to a
+ * multiple of 128; each column's 128 codes of one block share s = fp32(amax)/448
+ * (1 for zeros), q = e4m3_rne_satfinite(fp32(x / s)).  What lies behind the last
+ * group's last block is not written.  x, q_t 16-byte aligned. */
+moe_status moe_quantize_fp8_tokens(const uint16_t* x, const int32_t* offsets, int32_t G, int32_t M,
+                                   int32_t cols, uint8_t* q_t, float* scale_t, void* stream);
+
+/* Weight gradient of moe_gemm_fp8, dw[g] = dy_g^T x_g over the rows of each group:
+ *   dw[g][n][k] (+)= sum_b dy_t_scale[b][n] x_t_scale[b][k]
+ *                          * sum_{r = 128b}^{128b+127} dy_t[n][r] x_t[k][r]
+ * (b: the blocks of group g), dy_t [N][R] and x_t [K][R] as
+ * moe_quantize_fp8_tokens writes them for the same offsets and M.  dw [G][N][K]
+ * f32, added to when accumulate != 0, else written (zeros for a group without
+ * rows).  Limits as moe_gemm_fp8. */
+moe_status moe_gemm_fp8_wgrad(const uint8_t* dy_t, const float* dy_t_scale, const uint8_t* x_t,
+                              const float* x_t_scale, const int32_t* offsets, int32_t G, int32_t M,
+                              int32_t N, int32_t K, float* dw, int32_t accumulate, void* ws,
+                              size_t ws_bytes, void* stream);
 
 /* Synchronises `stream` and returns the device status word of `ws`
  * (MOE_OK, MOE_ERR_DEVICE_TIMEOUT or MOE_ERR_DEVICE_BAD_INDEX). */

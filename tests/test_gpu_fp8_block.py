@@ -1,0 +1,346 @@
+"""The FP8 block-128 product, its gradients and the token-block quantiser against
+their formulas in 64 bits on the codes' values.
+
+Tolerances: codes and scales exact (FP32 decides them on both sides); a product
+within train_ref.product_bound of the exact sum plus half a step of the output
+type (train_ref.HALF_STEP)."""
+import numpy as np
+import pytest
+import torch
+
+import train_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import expert_layer_dual_b200.moe as M
+
+DEV = "cuda"
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+def randn(shape, seed, scale=1.0, outliers=True):
+    x = torch.randn(shape, generator=torch.Generator().manual_seed(seed)) * scale
+    if outliers:
+        x[..., :: 37] *= 30.0
+    return x.to(torch.bfloat16)
+
+
+def offsets_of(sizes, first=0):
+    return torch.tensor(np.concatenate([[0], np.cumsum(sizes)]) + first, dtype=torch.int32)
+
+
+def workspace():
+    return torch.empty(256, dtype=torch.uint8, device=DEV)
+
+
+def check_rows(got, want, size, blocks, dtype):
+    got = got.double()
+    bound = ref.product_bound(size, blocks) + ref.HALF_STEP[dtype] * want.abs() + 2.0 ** -25 * (dtype == torch.float16)
+    err = (got - want).abs()
+    assert bool((err <= bound).all()), (float((err - bound).max()), float(err.max()))
+
+
+# sizes around every tile boundary: one row, a part of a tile, whole tiles, one row more
+DENSE = [(1, 128, 128), (1, 640, 2048), (2, 256, 384), (7, 1152, 256), (16, 512, 640), (17, 128, 1024),
+         (33, 384, 512), (63, 256, 896), (64, 2048, 128), (65, 768, 256), (100, 384, 384), (128, 128, 256),
+         (129, 256, 128), (200, 640, 640), (255, 256, 256), (256, 512, 512), (257, 384, 1152),
+         (300, 1280, 256), (513, 256, 2176), (700, 896, 128), (1025, 512, 384)]
+# (rows of each group, first row, rows behind the last group, N, K)
+GROUPED = [([5], 0, 0, 256, 128), ([0, 3, 0], 0, 0, 128, 256), ([1] * 9, 2, 5, 256, 256),
+           ([130, 0, 1, 256, 77], 0, 0, 384, 256), ([0, 0], 0, 40, 128, 128), ([300, 20, 500], 7, 9, 256, 640),
+           ([64, 64, 63, 65], 0, 0, 512, 384), ([3] * 256, 0, 0, 128, 128), ([0] * 100 + [400] + [0] * 60, 1, 1, 256, 256),
+           ([2, 700, 5, 0, 31, 16, 1], 3, 0, 640, 384), ([1100, 900], 0, 0, 384, 512)]
+
+
+def make_groups(sizes, first, behind):
+    rows = first + int(np.sum(sizes)) + behind
+    return rows, offsets_of(sizes, first)
+
+
+def product(op, rows, N, K, G, off, dtype, seed, stream=None):
+    """Runs the product on codes made on the CPU: (output on the CPU with a
+    sentinel behind unwritten rows, exact, magnitudes, covered)."""
+    a_cols, o_cols = (K, N) if op == "forward" else (N, K)
+    aq, a_s = ref.quantise_rows(randn((rows, a_cols), seed))
+    wq, ws = ref.quantise_weights(randn((G, N, K), seed + 1, 0.1))
+    out = torch.full((rows, o_cols), 7.0, dtype=dtype, device=DEV)
+    w = workspace()
+    f = M.gemm_fp8 if op == "forward" else M.gemm_fp8_dgrad
+    f(aq.to(DEV), a_s.to(DEV), (wq if off is not None else wq[0]).to(DEV),
+      (ws if off is not None else ws[0]).to(DEV), None if off is None else off.to(DEV), out, w, stream)
+    torch.cuda.synchronize()
+    assert M.read_device_status(w) == M.OK
+    want, size, covered = ref.grouped(ref.rows64(aq, a_s), ref.weights64(wq, ws), off, rows, op == "forward")
+    return out.cpu(), want, size, covered
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("op", ["forward", "input"])
+@pytest.mark.parametrize("shape", DENSE, ids=lambda s: "x".join(map(str, s)))
+def test_dense(shape, op, dtype):
+    rows, N, K = shape
+    got, want, size, _ = product(op, rows, N, K, 1, None, TYPES[dtype], rows + N)
+    check_rows(got, want, size, (K if op == "forward" else N) // 128, TYPES[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("op", ["forward", "input"])
+@pytest.mark.parametrize("case", range(len(GROUPED)))
+def test_grouped(case, op, dtype):
+    sizes, first, behind, N, K = GROUPED[case]
+    rows, off = make_groups(sizes, first, behind)
+    got, want, size, covered = product(op, rows, N, K, len(sizes), off, TYPES[dtype], case)
+    check_rows(got[covered], want[covered], size[covered], (K if op == "forward" else N) // 128, TYPES[dtype])
+    assert bool((got[~covered] == 7.0).all())
+
+
+@pytest.mark.parametrize("cols", [128, 384, 1024])
+@pytest.mark.parametrize("case", [None] + list(range(len(GROUPED))))
+def test_token_quantiser_exact(case, cols):
+    if case is None:
+        rows, off, G = 333, None, 1
+    else:
+        sizes, first, behind, _, _ = GROUPED[case]
+        rows, off = make_groups(sizes, first, behind)
+        G = len(sizes)
+    x = randn((rows, cols), 3 * cols)
+    x[:, 5] = 0
+    R = M.fp8_token_rows(rows, G)
+    q = torch.full((cols, R), 0x55, dtype=torch.uint8, device=DEV)
+    s = torch.full((R // 128, cols), -1.0, device=DEV)
+    M.quantize_fp8_tokens(x.to(DEV), None if off is None else off.to(DEV), q, s)
+    wq, ws, used = ref.quantise_tokens(x, off, R)
+    q, s = q.cpu(), s.cpu()
+    assert torch.equal(q[:, : used * 128], wq[:, : used * 128])
+    assert torch.equal(s[:used], ws[:used])
+    assert bool((q[:, used * 128:] == 0x55).all()) and bool((s[used:] == -1.0).all())
+
+
+def weight_gradient(rows, N, K, G, off, accumulate, seed):
+    dy, x = randn((rows, N), seed, 1e-3), randn((rows, K), seed + 1)
+    R = M.fp8_token_rows(rows, G)
+    offd = None if off is None else off.to(DEV)
+    ops = []
+    for t in (dy, x):
+        # what lies behind the groups' blocks is never read: poison it
+        q = torch.full((t.shape[1], R), 0x7F, dtype=torch.uint8, device=DEV)
+        s = torch.full((R // 128, t.shape[1]), float("nan"), device=DEV)
+        M.quantize_fp8_tokens(t.to(DEV), offd, q, s)
+        ops += [q, s]
+    start = randn((G, N, K), seed + 2, outliers=False).float()
+    dw = (start if off is not None else start[0]).to(DEV)
+    w = workspace()
+    M.gemm_fp8_wgrad(*ops, offd, rows, dw, accumulate, w)
+    torch.cuda.synchronize()
+    assert M.read_device_status(w) == M.OK
+    want, size = ref.weight_gradient(ops[0].cpu(), ops[1].cpu(), ops[2].cpu(), ops[3].cpu(), off, rows)
+    if accumulate:
+        want, size = want + start.double(), size + start.double().abs()
+    return dw.cpu().reshape(G, N, K), want, size
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("shape", DENSE, ids=lambda s: "x".join(map(str, s)))
+def test_weight_gradient_dense(shape, accumulate):
+    rows, N, K = shape
+    got, want, size = weight_gradient(rows, N, K, 1, None, accumulate, rows)
+    check_rows(got, want, size, (rows + 127) // 128, torch.float32)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("case", range(len(GROUPED)))
+def test_weight_gradient_grouped(case, accumulate):
+    sizes, first, behind, N, K = GROUPED[case]
+    if len(sizes) > 100:
+        N = K = 128
+    rows, off = make_groups(sizes, first, behind)
+    got, want, size = weight_gradient(rows, N, K, len(sizes), off, accumulate, case)
+    check_rows(got, want, size, max(1, (max(sizes) + 127) // 128), torch.float32)
+
+
+def test_no_rows():
+    w = workspace()
+    q = torch.empty((0, 128), dtype=torch.uint8, device=DEV)
+    s = torch.empty((0, 1), device=DEV)
+    wq, ws = ref.quantise_weights(randn((1, 128, 128), 1))
+    out = torch.empty((0, 128), device=DEV)
+    M.gemm_fp8(q, s, wq[0].to(DEV), ws[0].to(DEV), None, out, w)
+    t = torch.empty((128, 0), dtype=torch.uint8, device=DEV)
+    ts = torch.empty((0, 128), device=DEV)
+    M.quantize_fp8_tokens(torch.empty((0, 128), dtype=torch.bfloat16, device=DEV), None, t, ts)
+    dw = torch.ones((128, 128), device=DEV)
+    M.gemm_fp8_wgrad(t, ts, t, ts, None, 0, dw, True, w)
+    assert bool((dw == 1).all())
+    M.gemm_fp8_wgrad(t, ts, t, ts, None, 0, dw, False, w)
+    assert bool((dw == 0).all())
+
+
+def test_offsets_out_of_order_touch_nothing_outside():
+    """Offsets that no routing gives are clamped: a running maximum inside [0, M]."""
+    rows, N, K = 90, 128, 128
+    bad = torch.tensor([-5, 40, 20, 1000], dtype=torch.int32)
+    good = torch.tensor([0, 40, 40, 90], dtype=torch.int32)
+    aq, a_s = ref.quantise_rows(randn((rows, K), 1))
+    wq, ws = ref.quantise_weights(randn((3, N, K), 2))
+    outs = []
+    for off in (bad, good):
+        room = torch.full((rows + 64, N), 7.0, device=DEV)
+        M.gemm_fp8(aq.to(DEV), a_s.to(DEV), wq.to(DEV), ws.to(DEV), off.to(DEV), room[:rows], workspace())
+        assert bool((room[rows:] == 7.0).all())
+        outs.append(room[:rows].clone())
+    assert torch.equal(outs[0], outs[1])
+
+
+def test_f16_saturates():
+    rows, N, K = 3, 128, 256
+    aq, a_s = ref.quantise_rows(torch.full((rows, K), 300.0).to(torch.bfloat16))
+    wq, ws = ref.quantise_weights(torch.full((1, N, K), 2.0).to(torch.bfloat16))
+    out = torch.empty((rows, N), dtype=torch.float16, device=DEV)
+    M.gemm_fp8(aq.to(DEV), a_s.to(DEV), wq[0].to(DEV), ws[0].to(DEV), None, out, workspace())
+    assert bool((out == 65504.0).all())
+
+
+@pytest.mark.parametrize("shape", [(4, 256, 512), (400, 384, 256)])
+def test_infinite_scale_stays_in_its_row(shape):
+    """A NaN code or an infinite scale reaches its own row of y only."""
+    rows, N, K = shape
+    aq, a_s = ref.quantise_rows(randn((rows, K), 1))
+    wq, ws = ref.quantise_weights(randn((1, N, K), 2))
+    clean = torch.empty((rows, N), device=DEV)
+    args = (wq[0].to(DEV), ws[0].to(DEV), None)
+    M.gemm_fp8(aq.to(DEV), a_s.to(DEV), *args, clean, workspace())
+    aq[1, 3] = 0x7F
+    a_s[2, 1] = float("inf")
+    dirty = torch.empty((rows, N), device=DEV)
+    M.gemm_fp8(aq.to(DEV), a_s.to(DEV), *args, dirty, workspace())
+    keep = torch.ones(rows, dtype=torch.bool, device=DEV)
+    keep[1:3] = False
+    assert torch.equal(clean[keep], dirty[keep])
+    assert bool(torch.isnan(dirty[1]).all()) and not bool(torch.isfinite(dirty[2]).any())
+
+
+def test_capture_and_replay_on_a_side_stream():
+    """The whole step (quantise, product, both gradients) captured; two graphs with
+    one workspace, replayed in turn with new inputs, give the eager bits."""
+    rows, N, K, sizes = 500, 384, 256, [100, 0, 390, 10]
+    off = offsets_of(sizes).to(DEV)
+    G, R = len(sizes), M.fp8_token_rows(rows, len(sizes))
+    wq, ws = [t.to(DEV) for t in ref.quantise_weights(randn((G, N, K), 9, 0.1))]
+    shared = workspace()
+
+    def state(seed):
+        e = lambda *s, d=torch.uint8: torch.zeros(s, dtype=d, device=DEV)  # noqa: E731
+        return {"x": randn((rows, K), seed).to(DEV), "dy": randn((rows, N), seed + 1).to(DEV),
+                "xq": e(rows, K), "xs": e(rows, K // 128, d=torch.float32), "dq": e(rows, N),
+                "ds": e(rows, N // 128, d=torch.float32), "xt": e(K, R), "xts": e(R // 128, K, d=torch.float32),
+                "dt": e(N, R), "dts": e(R // 128, N, d=torch.float32), "y": e(rows, N, d=torch.bfloat16),
+                "dx": e(rows, K, d=torch.bfloat16), "dw": e(G, N, K, d=torch.float32)}
+
+    def step(s, w, stream=None):
+        M.quantize_act_fp8(s["x"], s["xq"], s["xs"], stream)
+        M.gemm_fp8(s["xq"], s["xs"], wq, ws, off, s["y"], w, stream)
+        M.quantize_act_fp8(s["dy"], s["dq"], s["ds"], stream)
+        M.gemm_fp8_dgrad(s["dq"], s["ds"], wq, ws, off, s["dx"], w, stream)
+        M.quantize_fp8_tokens(s["dy"], off, s["dt"], s["dts"], stream)
+        M.quantize_fp8_tokens(s["x"], off, s["xt"], s["xts"], stream)
+        M.gemm_fp8_wgrad(s["dt"], s["dts"], s["xt"], s["xts"], off, rows, s["dw"], False, w, stream)
+
+    a, b, fresh = state(1), state(3), state(5)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(st):
+        step(a, shared, st)
+        for s in (a, b):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=st):
+                step(s, shared, st)
+            graphs.append(g)
+        a["x"].copy_(fresh["x"])
+        a["dy"].copy_(fresh["dy"])
+        graphs[1].replay()
+        graphs[0].replay()
+    torch.cuda.current_stream().wait_stream(st)
+    torch.cuda.synchronize()
+    step(fresh, workspace())
+    eager_b = state(3)
+    step(eager_b, workspace())
+    torch.cuda.synchronize()
+    for k in ("y", "dx", "dw"):
+        assert torch.equal(a[k], fresh[k]) and torch.equal(b[k], eager_b[k]), k
+
+
+def test_two_streams_at_once():
+    """Two products in flight on two streams (a workspace each) give the bits of one."""
+    rows, N, K = 600, 640, 512
+    aq, a_s = [t.to(DEV) for t in ref.quantise_rows(randn((rows, K), 1))]
+    wq, ws = [t[0].to(DEV) for t in ref.quantise_weights(randn((1, N, K), 2))]
+    outs = [torch.empty((rows, N), dtype=torch.bfloat16, device=DEV) for _ in range(3)]
+    spaces = [workspace() for _ in range(3)]
+    M.gemm_fp8(aq, a_s, wq, ws, None, outs[2], spaces[2])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for i, st in enumerate(streams):
+            M.gemm_fp8(aq, a_s, wq, ws, None, outs[i], spaces[i], st)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
+
+
+def test_training_step_of_routed_experts():
+    """The operators together, as a routed FP8 projection is trained: top-k and
+    permute of the logits, x in the permuted order, the experts' product, the
+    gradients of the rows, the expert weights and the router's logits."""
+    T, E, k, N, K = 300, 12, 3, 256, 384
+    g = torch.Generator().manual_seed(6)
+    logits = torch.randn((T, E), generator=g) * 2
+    x, dy = randn((T, K), 7), randn((T * k, N), 8, 1e-2)
+    wq, ws = ref.quantise_weights(randn((E, N, K), 9, 0.1))
+    d = {n: t.to(DEV) for n, t in (("l", logits), ("x", x), ("dy", dy), ("wq", wq), ("ws", ws))}
+    i32 = lambda *s: torch.empty(s, dtype=torch.int32, device=DEV)  # noqa: E731
+    f32 = lambda *s: torch.empty(s, device=DEV)  # noqa: E731
+    u8 = lambda *s: torch.empty(s, dtype=torch.uint8, device=DEV)  # noqa: E731
+    ids, w, counts, off, perm, inv = i32(T, k), f32(T, k), i32(E), i32(E + 1), i32(T * k), i32(T * k)
+    M.route_topk(d["l"], k, True, ids, w)
+    M.permute(ids, E, counts, off, perm, inv, u8(M.permute_workspace_bytes(T, E, k)))
+    loss, bc, pm, tok, dl = f32(1), i32(E), f32(E), i32(1), f32(T, E)
+    M.balance_loss(d["l"], ids, None, 0.01, loss, bc, pm, tok, u8(M.balance_workspace_bytes(T, E)))
+    assert torch.equal(bc, counts)
+    R = T * k
+    xq, xs, y, sp = u8(R, K), f32(R, K // 128), torch.empty((R, N), dtype=torch.float16, device=DEV), workspace()
+    M.quantize_act_fp8_permuted(d["x"], perm, k, 0, xq, xs)
+    M.gemm_fp8(xq, xs, d["wq"], d["ws"], off, y, sp)
+    dq, ds, dx = u8(R, N), f32(R, N // 128), f32(R, K)
+    M.quantize_act_fp8(d["dy"], dq, ds)
+    M.gemm_fp8_dgrad(dq, ds, d["wq"], d["ws"], off, dx, sp)
+    rows = M.fp8_token_rows(R, E)
+    dt, dts, xt, xts, dw = u8(N, rows), f32(rows // 128, N), u8(K, rows), f32(rows // 128, K), f32(E, N, K)
+    xp = d["x"][(perm // k).long()].contiguous()
+    M.quantize_fp8_tokens(d["dy"], off, dt, dts)
+    M.quantize_fp8_tokens(xp, off, xt, xts)
+    M.gemm_fp8_wgrad(dt, dts, xt, xts, off, R, dw, False, sp)
+    # the gradient of w_j: <dy, y> of its row, then the router's logits
+    dwts = (d["dy"].float() * y.float()).sum(1)[inv.long()].reshape(T, k).contiguous()
+    one = torch.ones(1, device=DEV)
+    M.route_backward(d["l"], ids, w, dwts, None, True, one, 0.01, bc, tok, dl)
+    torch.cuda.synchronize()
+
+    offc, idc = off.cpu(), ids.cpu()
+    want = ref.balance(logits, idc, None, 0.01)
+    assert abs(float(loss.cpu()) - want["loss"]) <= 1e-5 * want["loss"]
+    W = ref.weights64(wq, ws)
+    yw, size, _ = ref.grouped(ref.rows64(xq.cpu(), xs.cpu()), W, offc, R, True)
+    check_rows(y.cpu(), yw, size, K // 128, torch.float16)
+    rq, rs = ref.quantise_rows(x[(perm.cpu() // k).long()])
+    assert torch.equal(rq, xq.cpu()) and torch.equal(rs, xs.cpu())
+    dxw, size, _ = ref.grouped(ref.rows64(dq.cpu(), ds.cpu()), W, offc, R, False)
+    check_rows(dx.cpu(), dxw, size, N // 128, torch.float32)
+    dww, size = ref.weight_gradient(dt.cpu(), dts.cpu(), xt.cpu(), xts.cpu(), offc, R)
+    check_rows(dw.cpu(), dww, size, int((counts.max() + 127) // 128), torch.float32)
+    dlw, size = ref.route_backward(logits, idc, w.cpu(), dwts.cpu(), None, True, 1.0, 0.01, want["counts"], T)
+    assert bool(((dl.cpu().double() - dlw).abs() <= 1e-5 * size + 1e-37).all())
+    # the adjoint identities on the values the codes stand for: <dy, y> = <dx, x>
+    lhs = float((ref.rows64(dq.cpu(), ds.cpu()) * yw).sum())
+    rhs = float((dxw * ref.rows64(xq.cpu(), xs.cpu())).sum())
+    assert abs(lhs - rhs) <= 1e-9 * float((dxw.abs() * ref.rows64(xq.cpu(), xs.cpu()).abs()).sum())

@@ -1056,8 +1056,6 @@ moe_status run_product(bool forward, const uint8_t* a, const float* a_scale, con
     p.out_type = out_type;
     p.status = at<int32_t>(ws, 0);
     p.timeout_ns = kDefaultTimeoutNs;
-    if (cudaMemsetAsync(p.status, 0, sizeof(int32_t), as_stream(stream)) != cudaSuccess)
-        return MOE_ERR_CUDA;
     return cuda_status((forward ? launch_gemm_fp8 : launch_gemm_fp8_dgrad)(p, as_stream(stream)));
 }
 }  // namespace
@@ -1127,8 +1125,6 @@ moe_status moe_gemm_fp8_wgrad(const uint8_t* dy_t, const float* dy_t_scale, cons
     p.accumulate = accumulate != 0 ? 1 : 0;
     p.status = at<int32_t>(ws, 0);
     p.timeout_ns = kDefaultTimeoutNs;
-    if (cudaMemsetAsync(p.status, 0, sizeof(int32_t), as_stream(stream)) != cudaSuccess)
-        return MOE_ERR_CUDA;
     return cuda_status(launch_gemm_fp8_wgrad(p, as_stream(stream)));
 }
 

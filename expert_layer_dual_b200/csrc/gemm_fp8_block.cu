@@ -17,29 +17,36 @@ namespace {
 enum Mode { kForward, kInput, kWeight };
 
 constexpr int BM = 128, PM = 256, BK = 128;    // rows of a CTA, of a pair; one scale block of the sum
-constexpr int H = 2, BN = 128 * H;             // output columns of a pair's tile
+constexpr int BN = 256;                        // output columns of a pair's tile
 constexpr int STAGES = 6, A_BYTES = BM * BK, B_BYTES = BN / 2 * BK, STAGE_BYTES = A_BYTES + B_BYTES;
-constexpr int NPART = 4;                       // partial buffers of 128 TMEM columns
+constexpr int NPART = 2;                       // partial buffers of BN TMEM columns
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int EPI_WARPS = 16, MMA_WARP = 16, A_WARP = 17, B_WARP = 18, SCALE_WARP = 19;
-constexpr int THREADS = 32 * (SCALE_WARP + 1);  // 640
+constexpr int EPI_WARPS = 16;                  // epilogue warps, EPI_COLS columns each
+constexpr int EPI_COLS = BN * 4 / EPI_WARPS;
+constexpr int MMA_WARP = EPI_WARPS, A_WARP = EPI_WARPS + 1, B_WARP = EPI_WARPS + 2,
+              SCALE_WARP = EPI_WARPS + 3;
+constexpr int THREADS = 32 * (SCALE_WARP + 1);
 // Registers: 640 threads x 96 at launch; the four helper warps fall to 32 and the
 // sixteen epilogue warps (64 accumulators each) rise to 112: 512 * 112 + 128 * 32
 // = 640 * 96 (checked against the compiled kernel before its first launch).
-constexpr int REGS = 96, REGS_EPI = 104, REGS_HELP = 64;
+constexpr int REGS = 96, REGS_EPI = 112, REGS_HELP = 32;
 constexpr int SC_KB = 4, SC_BUFS = 4;           // scales: chunks of 4 blocks, four chunks ahead
 constexpr uint16_t kPairMask = 0x3;
 
+// One chunk of scales, in floats: the CTA's 128 row scales of SC_KB blocks
+// ([row][block] for kForward and kInput, as they lie in memory; [block][row] for
+// kWeight), then the column side's: [block][2] weight scales, or [block][BN].
 template <Mode MODE>
-struct ScaleLayout {  // floats per block: the CTA's row scales, then the column side's
-    static constexpr int PER_KB = BM + (MODE == kWeight ? BN : 4);
-    static constexpr int FLOATS = SC_BUFS * SC_KB * PER_KB;
+struct ScaleLayout {
+    static constexpr int COLS = BM * SC_KB;  // where the column side's start
+    static constexpr int CHUNK = COLS + SC_KB * (MODE == kWeight ? BN : 4);
+    static constexpr int FLOATS = SC_BUFS * CHUNK;
 };
 
 struct Bars {
     uint64_t full[STAGES];      // leader: two arming arrivals (A and B) + both CTAs' bytes
-    uint64_t empty[STAGES];     // each CTA: the leader's multicast MMA commit
-    uint64_t pfull[NPART];      // each CTA: the leader's multicast MMA commit
+    uint64_t done[STAGES];      // each CTA: the leader's multicast MMA commit: the stage is
+                                // free and the block's partial is complete
     uint64_t pempty[NPART];     // leader: the warps of both CTAs that read the partial
     uint64_t sfull[SC_BUFS];    // scale chunk landed (32 asynchronous arrivals)
     uint64_t sempty[SC_BUFS];   // scale chunk read (one arrival per epilogue warp)
@@ -53,58 +60,120 @@ constexpr size_t smem_bytes() {
            sizeof(TileTable) + 64;
 }
 
+// The block's shared memory by 32-bit shared addresses (generic pointers cost
+// the loops registers they do not have).
 struct Smem {
-    uint8_t* stages;
-    float* scales;
-    Bars* bars;
+    uint32_t stages, scales, bars;
     TileTable* tt;
+    __device__ __forceinline__ uint32_t full(int i) const { return bars + offsetof(Bars, full) + 8 * i; }
+    __device__ __forceinline__ uint32_t done(int i) const { return bars + offsetof(Bars, done) + 8 * i; }
+    __device__ __forceinline__ uint32_t pempty(int i) const { return bars + offsetof(Bars, pempty) + 8 * i; }
+    __device__ __forceinline__ uint32_t sfull(int i) const { return bars + offsetof(Bars, sfull) + 8 * i; }
+    __device__ __forceinline__ uint32_t sempty(int i) const { return bars + offsetof(Bars, sempty) + 8 * i; }
+    __device__ __forceinline__ uint32_t abort_flag() const { return bars + offsetof(Bars, abort_flag); }
 };
 
-template <Mode MODE>
-__device__ __forceinline__ Smem carve(uint8_t* raw) {
-    Smem s;
-    s.stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) &
-                                          ~static_cast<uintptr_t>(1023));
-    s.scales = reinterpret_cast<float*>(s.stages + STAGES * STAGE_BYTES);
-    s.bars = reinterpret_cast<Bars*>(s.scales + ScaleLayout<MODE>::FLOATS);
-    s.tt = reinterpret_cast<TileTable*>(s.bars + 1);
-    return s;
+// ---------------------------------------------------------------- shared memory
+__device__ __forceinline__ float lds(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a));
+    return v;
+}
+__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, P;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
-// ---------------------------------------------------------------- bounded waits
-// A phase that is about to complete is met by the first tries, without a read of
-// the global timer; the time limit is kept by the slow loop.
-template <bool CLUSTER>
-__device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
-                                           const volatile int* abort) {
+// Bounded wait for a phase (see mbar_wait); the timer and the abort flag are read
+// once in 64 tries only.  It acquires at CTA scope in the leader too, whose
+// barriers take arrivals from both CTAs: what they order are asynchronous copies
+// (counted in bytes on the barrier) and TMEM reads, no generic memory write of
+// the other CTA.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
+                                           uint32_t abort_flag) {
+    uint64_t t0 = 0;
 #pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-        if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-    return CLUSTER ? mbar_wait_cluster(bar, parity, timeout_ns, abort)
-                   : mbar_wait(bar, parity, timeout_ns, abort);
+    for (uint32_t n = 1;; ++n) {
+        if (try_phase(bar, parity)) return true;
+        if ((n & 63u) == 0) {
+            int stop;
+            asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(stop) : "r"(abort_flag) : "memory");
+            const uint64_t t = global_timer_ns();
+            if (t0 == 0) t0 = t;
+            if (stop || t - t0 > timeout_ns) return false;
+        }
+    }
 }
 
-__device__ __forceinline__ bool warp_wait_phase(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
-                                                const volatile int* abort) {
-    return __all_sync(0xffffffffu, wait_phase<false>(bar, parity, timeout_ns, abort));
+// Warp-collective: one outcome for the warp.
+__device__ __forceinline__ bool warp_wait_phase(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
+                                                uint32_t abort_flag) {
+    return __all_sync(0xffffffffu, wait_phase(bar, parity, timeout_ns, abort_flag));
 }
 
-__device__ __forceinline__ void fail(Bars* b, int32_t* status) {
+// True in one lane of a converged warp.  The single-thread roles run their loops
+// with the whole warp and issue under this predicate: the operands then stay in
+// uniform registers (an MMA of N = 128 issued by `lane == 0` took 80 cycles, so
+// 64, the tensor core's own time).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+__device__ __forceinline__ void fail(const Smem& sm, int32_t* status) {
     report_status(status, MOE_ERR_DEVICE_TIMEOUT);
-    *reinterpret_cast<volatile int*>(&b->abort_flag) = 1;
+    asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(sm.abort_flag()) : "memory");
 }
 
-// One lane arrives on the leader's barrier.  Relaxed: what the barrier orders is
-// the reuse of TMEM columns, whose loads this warp has waited for; no memory
-// write travels with it, and a release at cluster scope would wait for the
-// warp's stores to global memory.
-__device__ __forceinline__ void warp_arrive_leader(uint64_t* bar) {
+// Shared::cluster address of shared address a in the pair's leader.
+__device__ __forceinline__ uint32_t in_leader(uint32_t a) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+    return r;
+}
+
+// One lane arrives on the leader's barrier (a cluster address).  Relaxed: what the
+// barrier orders is the reuse of TMEM columns, whose loads this warp has waited
+// for; no memory write travels with it, and a release at cluster scope would
+// wait for the warp's stores to global memory.
+__device__ __forceinline__ void warp_arrive_leader(uint32_t bar) {
     __syncwarp();
-    if ((threadIdx.x & 31) == 0)
-        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                         smem_in_rank(bar, 0))
+    if (elect_one())
+        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                      : "memory");
 }
+
+// A position in a ring of N slots: the slot and the parity of its round.
+template <int N>
+struct Ring {
+    uint32_t slot = 0, round = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            round ^= 1u;
+        }
+    }
+};
 
 // ---------------------------------------------------------------- operands
 // MMA of a CTA pair, e4m3.
@@ -114,6 +183,22 @@ __device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc,
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// umma_commit_pair and tma_load_2d_pair by shared addresses.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar),
+        "h"(kPairMask)
+        : "memory");
+}
+__device__ __forceinline__ void load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster,
+                                          int32_t x, int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
         : "memory");
 }
 // Instruction descriptor bit 16: B is stored with its N index innermost.
@@ -185,17 +270,123 @@ struct Work {
     }
 };
 
+// ---------------------------------------------------------------- scales
+__device__ __forceinline__ bool aligned16(const void* p) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+
+// The scale warp: keeps SC_BUFS chunks of SC_KB blocks' scales in flight ahead of
+// the epilogue (asynchronous copies that arrive on the chunk's barrier by
+// themselves).  16-byte copies where the layout allows (four blocks of a row, or
+// four columns, side by side and aligned), else 4-byte ones.  Rows and columns
+// past the tile read a neighbour's scale or, past the matrix, the last one: what
+// they scale is not stored.
+template <Mode MODE>
+__device__ __forceinline__ void scale_role(const Fp8ProductArgs& a, const Smem& sm, const Work<MODE>& work,
+                                        uint32_t rank, int pair, int npairs) {
+    using SL = ScaleLayout<MODE>;
+    const int lane = threadIdx.x & 31;
+    const int nb = a.N / 128, kbs = a.K / 128;
+    const int per_row = MODE == kForward ? kbs : nb;
+    const bool wide = MODE == kWeight ? aligned16(a.a_scale) && aligned16(a.b_scale)
+                                      : aligned16(a.a_scale) && per_row % 4 == 0;
+    Ring<SC_BUFS> ring;
+    bool ok = true;
+    for (int i = pair; ok && i < work.total; i += npairs) {
+        const PTile t = work.tile(a, sm.tt, i, rank);
+        for (int k0 = 0; k0 < t.blocks; k0 += SC_KB, ring.next()) {
+            if (!warp_wait_phase(sm.sempty(ring.slot), ring.round ^ 1u, a.timeout_ns, sm.abort_flag())) {
+                ok = false;
+                break;
+            }
+            const uint32_t dst = sm.scales + 4u * ring.slot * SL::CHUNK;
+            const int n = min(SC_KB, t.blocks - k0);
+            if (MODE == kWeight) {
+                for (int kk = 0; kk < n; ++kk) {
+                    const int64_t blk = t.block0 + k0 + kk;
+                    const float* ra = a.a_scale + blk * a.N;
+                    const float* cb = a.b_scale + blk * a.K;
+                    const uint32_t dr = dst + 4u * (kk * BM), dc = dst + 4u * (SL::COLS + kk * BN);
+                    if (wide) {
+                        const int r = lane * 4;
+                        cp_async_16(dr + 4u * r, ra + min(t.row0 + r, a.N - 4), 16u);
+#pragma unroll
+                        for (int c = lane * 4; c < BN; c += 128)
+                            cp_async_16(dc + 4u * c, cb + min(t.col0 + c, a.K - 4), 16u);
+                    } else {
+#pragma unroll 1
+                        for (int r = lane; r < BM; r += 32)
+                            cp_async_4(dr + 4u * r, ra + min(t.row0 + r, a.N - 1), 4u);
+#pragma unroll 1
+                        for (int c = lane; c < BN; c += 32)
+                            cp_async_4(dc + 4u * c, cb + min(t.col0 + c, a.K - 1), 4u);
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int r = lane; r < BM; r += 32) {
+                    const float* src = a.a_scale + (int64_t)min(t.row0 + r, a.M - 1) * per_row + k0;
+                    const uint32_t d = dst + 16u * r;
+                    if (wide) {
+                        cp_async_16(d, src, 16u);
+                    } else {
+#pragma unroll 1
+                        for (int kk = 0; kk < n; ++kk) cp_async_4(d + 4u * kk, src + kk, 4u);
+                    }
+                }
+                const int c = lane & 1, kk = lane >> 1;  // two column blocks x SC_KB
+                if (kk < n) {
+                    const int last = (MODE == kForward ? nb : kbs) - 1;
+                    const int col = min(t.col0 / 128 + c, last);
+                    const int64_t at = (int64_t)t.g * nb * kbs +
+                                       (MODE == kForward ? (int64_t)col * kbs + k0 + kk
+                                                         : (int64_t)(k0 + kk) * kbs + col);
+                    cp_async_4(dst + 4u * (SL::COLS + kk * 4 + c), a.b_scale + at, 4u);
+                }
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm.sfull(ring.slot))
+                         : "memory");
+        }
+    }
+    if (!ok && lane == 0) fail(sm, a.status);
+    cp_async_commit();
+    cp_async_wait<0>();
+}
+
 // ---------------------------------------------------------------- epilogue
-// acc += f * (32 TMEM columns), in pairs; with column scales: acc += f * (cs * P).
+#define R4(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3])
+#define W4(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3])
+// 32 FP32 columns of this thread's TMEM lane; complete after tmem_arrived.
+__device__ __forceinline__ void tmem_fetch32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : W4(r, 0), W4(r, 4), W4(r, 8), W4(r, 12), W4(r, 16), W4(r, 20), W4(r, 24), W4(r, 28)
+        : "r"(taddr)
+        : "memory");
+}
+// Waits for this thread's TMEM loads; names the registers, so that no use of them
+// can be scheduled before it.
+__device__ __forceinline__ void tmem_arrived(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : R4(r, 0), R4(r, 4), R4(r, 8), R4(r, 12), R4(r, 16), R4(r, 20), R4(r, 24), R4(r, 28)
+                 :
+                 : "memory");
+}
+#undef R4
+#undef W4
+
+// acc += f * (32 columns of the partial), in pairs; with column scales (at shared
+// address cs): f * (cs * P).
 template <bool COLSCALE>
-__device__ __forceinline__ void promote32(uint32_t taddr, uint64_t ff, const float* cs, uint64_t* acc) {
-    float v[32];
-    tmem_load32(taddr, v);
+__device__ __forceinline__ void promote32(const uint32_t* r, uint64_t ff, uint32_t cs, uint64_t* acc) {
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
-        uint64_t p0 = f32x2_pack(v[2 * i], v[2 * i + 1]), p1 = f32x2_pack(v[2 * i + 2], v[2 * i + 3]);
+        uint64_t p0 = f32x2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+        uint64_t p1 = f32x2_pack(__uint_as_float(r[2 * i + 2]), __uint_as_float(r[2 * i + 3]));
         if (COLSCALE) {
-            const float4 s = *reinterpret_cast<const float4*>(cs + 2 * i);
+            const float4 s = lds4(cs + 8 * i);
             p0 = f32x2_mul(p0, f32x2_pack(s.x, s.y));
             p1 = f32x2_mul(p1, f32x2_pack(s.z, s.w));
         }
@@ -240,34 +431,38 @@ __device__ __forceinline__ void store32(const Fp8ProductArgs& a, int64_t at, con
 
 // ---------------------------------------------------------------------------
 // The product on CTA pairs.  Per scale block of the summed index the pair
-// leader issues, for each half of the tile's 256 columns, four M = 256, N = 128,
-// K = 32 MMAs into a fresh 128-column partial (one of four in TMEM); the epilogue
-// warps take each partial out of TMEM and add it, scaled, to FP32 accumulators in
-// registers.  Half h holds columns 64h .. 64h+63 of the tile's two scale blocks
-// (CTA 0 loads the operand of the first block's columns, CTA 1 of the second's),
-// so a warp's 64 columns have one weight scale.
+// leader issues four M = 256, N = 256, K = 32 MMAs into a fresh partial (one of two
+// in TMEM) and one commit; the epilogue warps take each partial out of TMEM and
+// add it, scaled, to FP32 accumulators in registers while the next block's MMAs
+// run.  CTA 0 loads the operand of the tile's first 128 columns, CTA 1 of the
+// second, so a warp's columns have one weight scale.
+//
+// Measured, one pair per two SMs: four such MMAs take 512 cycles (the nominal
+// rate), and a commit to both CTAs 70 to 90 of its issuer's time, so a block has
+// one commit, which frees the stage and publishes the partial through the same
+// barrier.
 // ---------------------------------------------------------------------------
 template <Mode MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     k_product_pair(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                   Fp8ProductArgs a) {
+                   const __grid_constant__ Fp8ProductArgs a) {
     extern __shared__ uint8_t smem_raw[];
-    Smem sm = carve<MODE>(smem_raw);
-    Bars* b = sm.bars;
-    const volatile int* ab = &b->abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     using SL = ScaleLayout<MODE>;
+    Smem sm;
+    sm.stages = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    sm.scales = sm.stages + STAGES * STAGE_BYTES;
+    sm.bars = sm.scales + 4 * SL::FLOATS;
+    Bars* const b = reinterpret_cast<Bars*>(smem_raw + (sm.bars - smem_u32(smem_raw)));
+    sm.tt = reinterpret_cast<TileTable*>(b + 1);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&b->full[s], 2);
-            mbar_init(&b->empty[s], 1);
+            mbar_init(&b->done[s], 1);
         }
-        for (int i = 0; i < NPART; ++i) {
-            mbar_init(&b->pfull[i], 1);
-            mbar_init(&b->pempty[i], 2 * EPI_WARPS / H);
-        }
+        for (int i = 0; i < NPART; ++i) mbar_init(&b->pempty[i], 2 * EPI_WARPS);
         for (int i = 0; i < SC_BUFS; ++i) {
             mbar_init(&b->sfull[i], 32);
             mbar_init(&b->sempty[i], EPI_WARPS);
@@ -294,197 +489,158 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_HELP));
         if (warp == A_WARP || warp == B_WARP) {
             // ------------------------------------------------ TMA: one operand each
-            if (lane == 0) {
-                const bool is_a = warp == A_WARP;
-                const CUtensorMap* map = is_a ? &tm_a : &tm_b;
-                tma_prefetch_desc(map);
-                const uint32_t full_leader = smem_in_rank(&b->full[0], 0);
-                const uint32_t bytes = 2 * (is_a ? A_BYTES : B_BYTES);  // both CTAs'
-                uint8_t* dst0 = sm.stages + (is_a ? 0 : A_BYTES);
-                uint32_t it = 0;
-                bool ok = true;
-                for (int i = pair; ok && i < work.total; i += npairs) {
-                    const PTile t = work.tile(a, sm.tt, i, rank);
-                    const int col = t.col0 + (int)rank * (BN / 2);
-                    for (int kb = 0; kb < t.blocks; ++kb, ++it) {
-                        const int s = it % STAGES;
-                        if (!wait_phase<false>(&b->empty[s], ((it / STAGES) & 1) ^ 1, a.timeout_ns, ab)) {
-                            fail(b, a.status);
-                            ok = false;
-                            break;
-                        }
-                        if (rank == 0) mbar_arrive_expect_tx(&b->full[s], bytes);
-                        int x, y;
-                        if (is_a) {
-                            x = (t.block0 + kb) * BK;
-                            y = t.row0;
-                        } else if (MODE == kForward) {
-                            x = kb * BK;
-                            y = t.g * a.N + col;
-                        } else if (MODE == kInput) {
-                            x = col;
-                            y = t.g * a.N + kb * BK;
-                        } else {
-                            x = (t.block0 + kb) * BK;
-                            y = col;
-                        }
-                        tma_load_2d_pair(dst0 + s * STAGE_BYTES, map,
-                                         full_leader + s * (uint32_t)sizeof(uint64_t), x, y);
-                    }
-                }
-                // after a failure the pair's copies in flight are waited for (bounded)
-                if (*ab && rank == 0)
-                    for (uint32_t j = it > STAGES ? it - STAGES : 0; j < it; ++j)
-                        mbar_wait(&b->full[j % STAGES], (j / STAGES) & 1, a.timeout_ns, nullptr);
-            }
-        } else if (warp == MMA_WARP) {
-            // ------------------------------------------------ MMA issuer (leader)
-            if (lane == 0 && rank == 0) {
-                constexpr uint32_t idesc = idesc_e4m3(PM, 128) | (MODE == kInput ? kBTransposed : 0u);
-                uint32_t it = 0, pt = 0;
-                bool ok = true;
-                for (int i = pair; ok && i < work.total; i += npairs) {
-                    const int blocks = work.tile(a, sm.tt, i, 0).blocks;
-                    for (int kb = 0; ok && kb < blocks; ++kb, ++it) {
-                        const int s = it % STAGES;
-                        if (!wait_phase<true>(&b->full[s], (it / STAGES) & 1, a.timeout_ns, ab)) {
-                            fail(b, a.status);
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t sa = smem_u32(sm.stages + s * STAGE_BYTES), sb = sa + A_BYTES;
-#pragma unroll
-                        for (int h = 0; h < H; ++h, ++pt) {
-                            const uint32_t pb = pt % NPART;
-                            if (!wait_phase<true>(&b->pempty[pb], ((pt / NPART) & 1) ^ 1, a.timeout_ns,
-                                                  ab)) {
-                                fail(b, a.status);
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after_sync();
-#pragma unroll
-                            for (int kk = 0; kk < BK / 32; ++kk) {
-                                // K-major: half h starts 64 rows on, a K step 32 bytes on.
-                                // kInput: half h starts 64 bytes on in the rows (N innermost),
-                                // a K step 32 rows on.
-                                const uint32_t bo = MODE == kInput ? h * 64 + kk * 32 * 128
-                                                                   : h * 64 * 128 + kk * 32;
-                                umma_e4m3_pair(tmem + pb * 128, sdesc_k_sw128(sa + kk * 32),
-                                               sdesc_k_sw128(sb + bo), idesc, kk != 0);
-                            }
-                            umma_commit_pair(&b->pfull[pb], kPairMask);
-                        }
-                        umma_commit_pair(&b->empty[s], kPairMask);
-                    }
-                }
-            }
-        } else {
-            // ------------------------------------------------ scales, SC_KB blocks at a time
-            const float* row_scale = a.a_scale;
-            uint32_t cc = 0;
+            const bool is_a = warp == A_WARP;
+            const CUtensorMap* map = is_a ? &tm_a : &tm_b;
+            if (elect_one()) tma_prefetch_desc(map);
+            const uint32_t full_leader = in_leader(sm.full(0));
+            const uint32_t bytes = 2 * (is_a ? A_BYTES : B_BYTES);  // both CTAs'
+            const uint32_t dst0 = sm.stages + (is_a ? 0 : A_BYTES);
+            Ring<STAGES> st;
+            uint32_t issued = 0;
             bool ok = true;
             for (int i = pair; ok && i < work.total; i += npairs) {
                 const PTile t = work.tile(a, sm.tt, i, rank);
-                const int nb = a.N / 128, kbs = a.K / 128;
-                for (int k0 = 0; k0 < t.blocks; k0 += SC_KB, ++cc) {
-                    const int buf = cc % SC_BUFS;
-                    if (!warp_wait_phase(&b->sempty[buf], ((cc / SC_BUFS) & 1) ^ 1, a.timeout_ns, ab)) {
+                const int col = t.col0 + (int)rank * (BN / 2);
+                int x, y;  // of the tile's first block
+                if (is_a) {
+                    x = t.block0 * BK;
+                    y = t.row0;
+                } else if (MODE == kForward) {
+                    x = 0;
+                    y = t.g * a.N + col;
+                } else if (MODE == kInput) {
+                    x = col;
+                    y = t.g * a.N;
+                } else {
+                    x = t.block0 * BK;
+                    y = col;
+                }
+                for (int kb = 0; kb < t.blocks; ++kb, st.next()) {
+                    if (!warp_wait_phase(sm.done(st.slot), st.round ^ 1u, a.timeout_ns, sm.abort_flag())) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = smem_u32(sm.scales + buf * SC_KB * SL::PER_KB);
-                    const int n = min(SC_KB, t.blocks - k0);
-                    if (MODE == kWeight) {
-                        for (int kk = 0; kk < n; ++kk) {
-                            const int64_t blk = t.block0 + k0 + kk;
-                            for (int r = lane; r < BM; r += 32)
-                                cp_async_4(dst + 4u * (kk * SL::PER_KB + r),
-                                           row_scale + blk * a.N + min(t.row0 + r, a.N - 1), 4u);
-                            for (int c = lane; c < BN; c += 32)
-                                cp_async_4(dst + 4u * (kk * SL::PER_KB + BM + c),
-                                           a.b_scale + blk * a.K + min(t.col0 + c, a.K - 1), 4u);
-                        }
-                    } else {
-                        const int per_row = MODE == kForward ? kbs : nb;
-                        for (int j = lane; j < BM * SC_KB; j += 32) {
-                            const int r = j / SC_KB, kk = j % SC_KB;
-                            if (kk < n) {
-                                const bool in = r < t.nrows;
-                                cp_async_4(dst + 4u * (kk * SL::PER_KB + r),
-                                           row_scale + (in ? (int64_t)(t.row0 + r) * per_row + k0 + kk : 0),
-                                           in ? 4u : 0u);
-                            }
-                        }
-                        const int c = lane & 1, kk = lane >> 1;  // two column blocks x SC_KB
-                        if (kk < n) {
-                            const int last = (MODE == kForward ? nb : kbs) - 1;
-                            const int cb = min(t.col0 / 128 + c, last);
-                            const int64_t at = (int64_t)t.g * nb * kbs +
-                                               (MODE == kForward ? (int64_t)cb * kbs + k0 + kk
-                                                                 : (int64_t)(k0 + kk) * kbs + cb);
-                            cp_async_4(dst + 4u * (kk * SL::PER_KB + BM + c), a.b_scale + at, 4u);
-                        }
+                    if (elect_one()) {
+                        if (rank == 0)
+                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
+                                             sm.full(st.slot)),
+                                         "r"(bytes)
+                                         : "memory");
+                        load_pair(dst0 + st.slot * STAGE_BYTES, map, full_leader + 8 * st.slot, x, y);
                     }
-                    cp_async_mbar_arrive_noinc(&b->sfull[buf]);
+                    __syncwarp();
+                    ++issued;
+                    if (MODE == kInput && !is_a) y += BK; else x += BK;
                 }
             }
-            if (!ok && lane == 0) fail(b, a.status);
-            cp_async_commit();
-            cp_async_wait<0>();
+            if (!ok && lane == 0) fail(sm, a.status);
+            // after a failure the pair's copies in flight are waited for (bounded)
+            if (rank == 0 && lane == 0 && *reinterpret_cast<volatile int*>(&b->abort_flag))
+                for (uint32_t j = issued > STAGES ? issued - STAGES : 0; j < issued; ++j)
+                    mbar_wait(&b->full[j % STAGES], (j / STAGES) & 1, a.timeout_ns, nullptr);
+        } else if (warp == MMA_WARP) {
+            // ------------------------------------------------ MMA issuer (leader)
+            if (rank == 0) {
+                constexpr uint32_t idesc = idesc_e4m3(PM, BN) | (MODE == kInput ? kBTransposed : 0u);
+                Ring<STAGES> st;
+                Ring<NPART> pt;
+                bool ok = true;
+                for (int i = pair; ok && i < work.total; i += npairs) {
+                    const int blocks = work.tile(a, sm.tt, i, 0).blocks;
+                    for (int kb = 0; kb < blocks; ++kb, st.next(), pt.next()) {
+                        if (!warp_wait_phase(sm.full(st.slot), st.round, a.timeout_ns, sm.abort_flag()) ||
+                            !warp_wait_phase(sm.pempty(pt.slot), pt.round ^ 1u, a.timeout_ns,
+                                             sm.abort_flag())) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after_sync();
+                        const uint32_t sa = sm.stages + st.slot * STAGE_BYTES, sb = sa + A_BYTES;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 0; kk < BK / 32; ++kk)
+                                // a K step: 32 bytes on (K innermost), or 32 rows on (kInput)
+                                umma_e4m3_pair(tmem + pt.slot * BN, sdesc_k_sw128(sa + kk * 32),
+                                               sdesc_k_sw128(sb + (MODE == kInput ? kk * 32 * 128 : kk * 32)),
+                                               idesc, kk != 0);
+                            commit_pair(sm.done(st.slot));
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (!ok && lane == 0) fail(sm, a.status);
+            }
+        } else {
+            // ------------------------------------------------ scales, SC_KB blocks at a time
+            scale_role<MODE>(a, sm, work, rank, pair, npairs);
         }
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
         // ---------------------------------------------------- promotion and output
-        const int quad = warp & 3, half = (warp >> 2) & 1, cb = warp >> 3;
+        const int quad = warp & 3, part = warp >> 2;  // TMEM lanes, columns
         const int row = quad * 32 + lane;
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + cb * 64;
-        uint32_t pt = half, cc = 0;
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * EPI_COLS;
+        const uint32_t pempty_leader = in_leader(sm.pempty(0));
+        constexpr bool CS = MODE == kWeight;
+        constexpr int NQ = EPI_COLS / 32;
+        Ring<STAGES> st;
+        Ring<SC_BUFS> ch;
+        uint32_t pb = 0;
         bool ok = true;
         for (int i = pair; ok && i < work.total; i += npairs) {
-            const PTile t = work.tile(a, sm.tt, i, rank);
-            uint64_t acc[32];
+            const int blocks = work.tile(a, sm.tt, i, rank).blocks;
+            uint64_t acc[16 * NQ];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[j] = 0ull;
+            for (int j = 0; j < 16 * NQ; ++j) acc[j] = 0ull;
 #pragma unroll 1
-            for (int kb = 0; kb < t.blocks; ++kb, pt += H) {
-                const int kk = kb % SC_KB, buf = cc % SC_BUFS;
-                if (kk == 0 &&
-                    !warp_wait_phase(&b->sfull[buf], (cc / SC_BUFS) & 1, a.timeout_ns, ab)) {
+            for (int kb = 0; kb < blocks; ++kb) {
+                const int kk = kb % SC_KB;
+                if (kk == 0 && !warp_wait_phase(sm.sfull(ch.slot), ch.round, a.timeout_ns, sm.abort_flag())) {
                     ok = false;
                     break;
                 }
-                const float* sc = sm.scales + (buf * SC_KB + kk) * SL::PER_KB;
-                float f = sc[row];
-                if (MODE != kWeight) f *= sc[BM + cb];
+                const uint32_t sc = sm.scales + 4u * ch.slot * SL::CHUNK;
+                float f = lds(sc + 4u * (CS ? kk * BM + row : row * SC_KB + kk));
+                if (!CS) f *= lds(sc + 4u * (SL::COLS + kk * 4 + part * EPI_COLS / 128));
                 const uint64_t ff = f32x2_pack(f, f);
-                const uint32_t pb = pt % NPART;
-                if (!warp_wait_phase(&b->pfull[pb], (pt / NPART) & 1, a.timeout_ns, ab)) {
+                const uint32_t cs = sc + 4u * (SL::COLS + kk * BN + part * EPI_COLS);
+                if (!warp_wait_phase(sm.done(st.slot), st.round, a.timeout_ns, sm.abort_flag())) {
                     ok = false;
                     break;
                 }
                 tc_fence_after_sync();
-                const float* cs = sc + BM + cb * 128 + half * 64;
-                promote32<MODE == kWeight>(taddr + pb * 128, ff, cs, acc);
-                promote32<MODE == kWeight>(taddr + pb * 128 + 32, ff, cs + 32, acc + 16);
-                tc_fence_before_sync();
-                warp_arrive_leader(&b->pempty[pb]);
-                if (kk == SC_KB - 1 || kb == t.blocks - 1) {
-                    if (lane == 0) mbar_arrive(&b->sempty[buf]);
-                    ++cc;
+                uint32_t r[32];
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    tmem_fetch32(taddr + pb * BN + 32 * q, r);
+                    tmem_arrived(r);
+                    if (q == NQ - 1) {  // the partial is in registers
+                        tc_fence_before_sync();
+                        warp_arrive_leader(pempty_leader + 8 * pb);
+                    }
+                    promote32<CS>(r, ff, cs + 128 * q, acc + 16 * q);
+                }
+                st.next();
+                pb ^= 1u;
+                if (kk == SC_KB - 1 || kb == blocks - 1) {
+                    __syncwarp();
+                    if (elect_one()) arrive(sm.sempty(ch.slot));
+                    ch.next();
                 }
             }
             if (!ok) {
-                if (lane == 0) fail(b, a.status);
+                if (lane == 0) fail(sm, a.status);
                 break;
             }
+            // decoded again rather than kept: the loop has no registers to spare
+            const PTile t = work.tile(a, sm.tt, i, rank);
             const int cols = MODE == kForward ? a.N : a.K;
-            const int col = t.col0 + cb * 128 + half * 64;
+            const int col = t.col0 + part * EPI_COLS;
             if (row < t.nrows && col < cols && !(MODE == kWeight && a.accumulate && t.blocks == 0)) {
                 const int64_t r = MODE == kWeight ? (int64_t)t.g * a.N + t.row0 + row : t.row0 + row;
-                store32<MODE>(a, r * cols + col, acc);
-                store32<MODE>(a, r * cols + col + 32, acc + 16);
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) store32<MODE>(a, r * cols + col + 32 * q, acc + 16 * q);
             }
             __syncwarp();
         }

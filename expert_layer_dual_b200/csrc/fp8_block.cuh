@@ -1,5 +1,5 @@
-// fp8_block.cuh -- shared by the FP8 block-128 product, its gradients and the
-// token-block quantiser: the group table of a row matrix.
+// fp8_block.cuh -- shared by the FP8 block-128 products and the token-block
+// quantiser: the group table of a row matrix, and device helpers.
 #pragma once
 
 #include "grouped_common.cuh"
@@ -74,16 +74,163 @@ __device__ __forceinline__ int group_of(const TileTable* tt, int G, int tile) {
     return lo;
 }
 
-// The output types of the products.
-__device__ __forceinline__ void store_out(void* out, int64_t i, float v, int type) {
-    if (type == MOE_OUT_F32) {
-        static_cast<float*>(out)[i] = v;
-    } else if (type == MOE_OUT_F16) {
-        const uint32_t h = pack_f16x2_sat(v, 0.0f);
-        static_cast<uint16_t*>(out)[i] = (uint16_t)h;
-    } else {
-        static_cast<__nv_bfloat16*>(out)[i] = __float2bfloat16_rn(v);
+// ---------------------------------------------------------------- device helpers
+// Shared memory is addressed by 32-bit shared addresses: generic pointers cost
+// the promotion loops registers that they do not have.
+__device__ __forceinline__ float lds(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a));
+    return v;
+}
+__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
+        "selp.b32 %0, 1, 0, P;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Bounded wait for a phase (see mbar_wait); the timer and the abort flag are read
+// once in 64 tries only.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
+                                           uint32_t abort_flag) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t n = 1;; ++n) {
+        if (try_phase(bar, parity)) return true;
+        if ((n & 63u) == 0) {
+            int stop;
+            asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(stop) : "r"(abort_flag) : "memory");
+            const uint64_t t = global_timer_ns();
+            if (t0 == 0) t0 = t;
+            if (stop || t - t0 > timeout_ns) return false;
+        }
     }
+}
+
+// Warp-collective: one outcome for the warp.
+__device__ __forceinline__ bool warp_wait_phase(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
+                                                uint32_t abort_flag) {
+    return __all_sync(0xffffffffu, wait_phase(bar, parity, timeout_ns, abort_flag));
+}
+
+// True in one lane of a converged warp.  The single-thread roles run their loops
+// with the whole warp and issue under this predicate: the operands then stay in
+// uniform registers.  Measured: an MMA of N = 128 issued by `lane == 0` took 80
+// cycles, issued so 64, the tensor core's own time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x,
+                                         int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+// Shared-memory descriptor of an operand stored with its M (or N) index innermost
+// and the 128-byte swizzle: each row of 128 bytes holds 128 of the index at one k,
+// groups of eight k are 1024 bytes apart (stride field), the next 128 of the
+// index `next` bytes on (leading field).
+__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t next) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>((next >> 4) & 0x3FFFu) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+// Instruction descriptor bits 15 and 16: A, B stored with M, N innermost.
+constexpr uint32_t kATransposed = 1u << 15, kBTransposed = 1u << 16;
+
+// A position in a ring of N slots: the slot and the parity of its round.
+template <int N>
+struct Ring {
+    uint32_t slot = 0, round = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            round ^= 1u;
+        }
+    }
+};
+
+
+__device__ __forceinline__ uint64_t f32x2_pack(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f32x2_unpack(uint64_t r, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
+}
+__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+#define R4(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3])
+#define W4(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3])
+// 32 FP32 columns of this thread's TMEM lane; complete after tmem_arrived.
+__device__ __forceinline__ void tmem_fetch32(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : W4(r, 0), W4(r, 4), W4(r, 8), W4(r, 12), W4(r, 16), W4(r, 20), W4(r, 24), W4(r, 28)
+        : "r"(taddr)
+        : "memory");
+}
+// Waits for this thread's TMEM loads; names the registers, so that no use of them
+// can be scheduled before it.
+__device__ __forceinline__ void tmem_arrived(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : R4(r, 0), R4(r, 4), R4(r, 8), R4(r, 12), R4(r, 16), R4(r, 20), R4(r, 24), R4(r, 28)
+                 :
+                 : "memory");
+}
+#undef R4
+#undef W4
+
+__device__ __forceinline__ bool aligned16(const void* p) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
 }  // namespace moe

@@ -16,9 +16,8 @@ namespace {
 
 enum Mode { kForward, kInput, kWeight };
 
-constexpr int BM = 128, PM = 256, BK = 128;    // rows of a CTA, of a pair; one scale block of the sum
-constexpr int BN = 256;                        // output columns of a pair's tile
-constexpr int STAGES = 6, A_BYTES = BM * BK, B_BYTES = BN / 2 * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int BM = 128, BN = 256, BK = 128;    // a tile's rows and columns; one scale block of the sum
+constexpr int STAGES = 4, A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int NPART = 2;                       // partial buffers of BN TMEM columns
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int EPI_WARPS = 16;                  // epilogue warps, EPI_COLS columns each
@@ -31,7 +30,6 @@ constexpr int THREADS = 32 * (SCALE_WARP + 1);
 // = 640 * 96 (checked against the compiled kernel before its first launch).
 constexpr int REGS = 96, REGS_EPI = 112, REGS_HELP = 32;
 constexpr int SC_KB = 4, SC_BUFS = 4;           // scales: chunks of 4 blocks, four chunks ahead
-constexpr uint16_t kPairMask = 0x3;
 
 // One chunk of scales, in floats: the CTA's 128 row scales of SC_KB blocks
 // ([row][block] for kForward and kInput, as they lie in memory; [block][row] for
@@ -44,10 +42,9 @@ struct ScaleLayout {
 };
 
 struct Bars {
-    uint64_t full[STAGES];      // leader: two arming arrivals (A and B) + both CTAs' bytes
-    uint64_t done[STAGES];      // each CTA: the leader's multicast MMA commit: the stage is
-                                // free and the block's partial is complete
-    uint64_t pempty[NPART];     // leader: the warps of both CTAs that read the partial
+    uint64_t full[STAGES];      // two arming arrivals (A and B) + their bytes
+    uint64_t done[STAGES];      // MMA commit: the stage is free, the block's partial complete
+    uint64_t pempty[NPART];     // partial read (one arrival per epilogue warp)
     uint64_t sfull[SC_BUFS];    // scale chunk landed (32 asynchronous arrivals)
     uint64_t sempty[SC_BUFS];   // scale chunk read (one arrival per epilogue warp)
     uint32_t tmem_slot;
@@ -60,8 +57,7 @@ constexpr size_t smem_bytes() {
            sizeof(TileTable) + 64;
 }
 
-// The block's shared memory by 32-bit shared addresses (generic pointers cost
-// the loops registers they do not have).
+// The block's shared memory, by shared addresses.
 struct Smem {
     uint32_t stages, scales, bars;
     TileTable* tt;
@@ -73,160 +69,15 @@ struct Smem {
     __device__ __forceinline__ uint32_t abort_flag() const { return bars + offsetof(Bars, abort_flag); }
 };
 
-// ---------------------------------------------------------------- shared memory
-__device__ __forceinline__ float lds(uint32_t a) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ float4 lds4(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(a));
-    return v;
-}
-__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred P;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n\t"
-        "selp.b32 %0, 1, 0, P;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-__device__ __forceinline__ void arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-// Bounded wait for a phase (see mbar_wait); the timer and the abort flag are read
-// once in 64 tries only.  It acquires at CTA scope in the leader too, whose
-// barriers take arrivals from both CTAs: what they order are asynchronous copies
-// (counted in bytes on the barrier) and TMEM reads, no generic memory write of
-// the other CTA.
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
-                                           uint32_t abort_flag) {
-    uint64_t t0 = 0;
-#pragma unroll 1
-    for (uint32_t n = 1;; ++n) {
-        if (try_phase(bar, parity)) return true;
-        if ((n & 63u) == 0) {
-            int stop;
-            asm volatile("ld.volatile.shared.s32 %0, [%1];" : "=r"(stop) : "r"(abort_flag) : "memory");
-            const uint64_t t = global_timer_ns();
-            if (t0 == 0) t0 = t;
-            if (stop || t - t0 > timeout_ns) return false;
-        }
-    }
-}
-
-// Warp-collective: one outcome for the warp.
-__device__ __forceinline__ bool warp_wait_phase(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
-                                                uint32_t abort_flag) {
-    return __all_sync(0xffffffffu, wait_phase(bar, parity, timeout_ns, abort_flag));
-}
-
-// True in one lane of a converged warp.  The single-thread roles run their loops
-// with the whole warp and issue under this predicate: the operands then stay in
-// uniform registers (an MMA of N = 128 issued by `lane == 0` took 80 cycles, so
-// 64, the tensor core's own time).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile(
-        "{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.b32 %0, 1, 0, P;\n\t}"
-        : "=r"(p));
-    return p != 0;
-}
-
 __device__ __forceinline__ void fail(const Smem& sm, int32_t* status) {
     report_status(status, MOE_ERR_DEVICE_TIMEOUT);
     asm volatile("st.volatile.shared.s32 [%0], 1;" ::"r"(sm.abort_flag()) : "memory");
 }
 
-// Shared::cluster address of shared address a in the pair's leader.
-__device__ __forceinline__ uint32_t in_leader(uint32_t a) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
-    return r;
-}
-
-// One lane arrives on the leader's barrier (a cluster address).  Relaxed: what the
-// barrier orders is the reuse of TMEM columns, whose loads this warp has waited
-// for; no memory write travels with it, and a release at cluster scope would
-// wait for the warp's stores to global memory.
-__device__ __forceinline__ void warp_arrive_leader(uint32_t bar) {
-    __syncwarp();
-    if (elect_one())
-        asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                     : "memory");
-}
-
-// A position in a ring of N slots: the slot and the parity of its round.
-template <int N>
-struct Ring {
-    uint32_t slot = 0, round = 0;
-    __device__ __forceinline__ void next() {
-        if (++slot == N) {
-            slot = 0;
-            round ^= 1u;
-        }
-    }
-};
-
-// ---------------------------------------------------------------- operands
-// MMA of a CTA pair, e4m3.
-__device__ __forceinline__ void umma_e4m3_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                               uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// umma_commit_pair and tma_load_2d_pair by shared addresses.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-        " [%0], %1;" ::"r"(bar),
-        "h"(kPairMask)
-        : "memory");
-}
-__device__ __forceinline__ void load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster,
-                                          int32_t x, int32_t y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y)
-        : "memory");
-}
-// Instruction descriptor bit 16: B is stored with its N index innermost.
-constexpr uint32_t kBTransposed = 1u << 16;
-
-__device__ __forceinline__ uint64_t f32x2_pack(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void f32x2_unpack(uint64_t r, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(r));
-}
-__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // ---------------------------------------------------------------- tiles
-// One tile of a pair: rows row0 .. of the output (this CTA's 128 of 256), columns
-// col0 .., group g, and the scale blocks [block0, block0 + blocks) that it sums
-// over (kWeight: token blocks of the group; else all of them, from 0).
+// One tile: rows row0 .. (nrows <= 128) and columns col0 .. (256) of the output, group
+// g, and the scale blocks [block0, block0 + blocks) that it sums over (kWeight:
+// token blocks of the group; else all of them, from 0).
 struct PTile {
     int g, row0, nrows, col0, block0, blocks;
 };
@@ -237,7 +88,7 @@ struct Work {
     __device__ __forceinline__ Work(const Fp8ProductArgs& a, const TileTable* tt) {
         if (MODE == kWeight) {
             n_tiles = (a.K + BN - 1) / BN;
-            k_tiles = (a.N + PM - 1) / PM;
+            k_tiles = a.N / BM;
             total = a.G * n_tiles * k_tiles;
         } else {
             n_tiles = ((MODE == kForward ? a.N : a.K) + BN - 1) / BN;
@@ -245,23 +96,22 @@ struct Work {
             total = tt->mstart[a.G] * n_tiles;
         }
     }
-    __device__ __forceinline__ PTile tile(const Fp8ProductArgs& a, const TileTable* tt, int i,
-                                          uint32_t rank) const {
+    __device__ __forceinline__ PTile tile(const Fp8ProductArgs& a, const TileTable* tt, int i) const {
         PTile p;
         if (MODE == kWeight) {
             const int per = n_tiles * k_tiles;
             p.g = i / per;
             const int r = i - p.g * per;
-            p.row0 = (r / n_tiles) * PM + (int)rank * BM;
-            p.nrows = min(BM, max(0, a.N - p.row0));
+            p.row0 = (r / n_tiles) * BM;
+            p.nrows = BM;
             p.col0 = (r % n_tiles) * BN;
             p.block0 = tt->mstart[p.g];
             p.blocks = tt->mstart[p.g + 1] - p.block0;
         } else {
-            const Tile t = decode_tile(tt, a.G, n_tiles, i, PM);
+            const Tile t = decode_tile(tt, a.G, n_tiles, i, BM);
             p.g = t.g;
-            p.row0 = t.row0 + (int)rank * BM;
-            p.nrows = min(BM, max(0, t.nrows - (int)rank * BM));
+            p.row0 = t.row0;
+            p.nrows = t.nrows;
             p.col0 = t.n * BN;
             p.block0 = 0;
             p.blocks = blocks;
@@ -271,10 +121,6 @@ struct Work {
 };
 
 // ---------------------------------------------------------------- scales
-__device__ __forceinline__ bool aligned16(const void* p) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
-}
-
 // The scale warp: keeps SC_BUFS chunks of SC_KB blocks' scales in flight ahead of
 // the epilogue (asynchronous copies that arrive on the chunk's barrier by
 // themselves).  16-byte copies where the layout allows (four blocks of a row, or
@@ -282,8 +128,7 @@ __device__ __forceinline__ bool aligned16(const void* p) {
 // past the tile read a neighbour's scale or, past the matrix, the last one: what
 // they scale is not stored.
 template <Mode MODE>
-__device__ __forceinline__ void scale_role(const Fp8ProductArgs& a, const Smem& sm, const Work<MODE>& work,
-                                        uint32_t rank, int pair, int npairs) {
+__device__ __forceinline__ void scale_role(const Fp8ProductArgs& a, const Smem& sm, const Work<MODE>& work) {
     using SL = ScaleLayout<MODE>;
     const int lane = threadIdx.x & 31;
     const int nb = a.N / 128, kbs = a.K / 128;
@@ -292,8 +137,8 @@ __device__ __forceinline__ void scale_role(const Fp8ProductArgs& a, const Smem& 
                                       : aligned16(a.a_scale) && per_row % 4 == 0;
     Ring<SC_BUFS> ring;
     bool ok = true;
-    for (int i = pair; ok && i < work.total; i += npairs) {
-        const PTile t = work.tile(a, sm.tt, i, rank);
+    for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
+        const PTile t = work.tile(a, sm.tt, i);
         for (int k0 = 0; k0 < t.blocks; k0 += SC_KB, ring.next()) {
             if (!warp_wait_phase(sm.sempty(ring.slot), ring.round ^ 1u, a.timeout_ns, sm.abort_flag())) {
                 ok = false;
@@ -354,29 +199,6 @@ __device__ __forceinline__ void scale_role(const Fp8ProductArgs& a, const Smem& 
 }
 
 // ---------------------------------------------------------------- epilogue
-#define R4(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3])
-#define W4(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3])
-// 32 FP32 columns of this thread's TMEM lane; complete after tmem_arrived.
-__device__ __forceinline__ void tmem_fetch32(uint32_t taddr, uint32_t* r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : W4(r, 0), W4(r, 4), W4(r, 8), W4(r, 12), W4(r, 16), W4(r, 20), W4(r, 24), W4(r, 28)
-        : "r"(taddr)
-        : "memory");
-}
-// Waits for this thread's TMEM loads; names the registers, so that no use of them
-// can be scheduled before it.
-__device__ __forceinline__ void tmem_arrived(uint32_t* r) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : R4(r, 0), R4(r, 4), R4(r, 8), R4(r, 12), R4(r, 16), R4(r, 20), R4(r, 24), R4(r, 28)
-                 :
-                 : "memory");
-}
-#undef R4
-#undef W4
-
 // acc += f * (32 columns of the partial), in pairs; with column scales (at shared
 // address cs): f * (cs * P).
 template <bool COLSCALE>
@@ -430,25 +252,27 @@ __device__ __forceinline__ void store32(const Fp8ProductArgs& a, int64_t at, con
 }
 
 // ---------------------------------------------------------------------------
-// The product on CTA pairs.  Per scale block of the summed index the pair
-// leader issues four M = 256, N = 256, K = 32 MMAs into a fresh partial (one of two
-// in TMEM) and one commit; the epilogue warps take each partial out of TMEM and
-// add it, scaled, to FP32 accumulators in registers while the next block's MMAs
-// run.  CTA 0 loads the operand of the tile's first 128 columns, CTA 1 of the
-// second, so a warp's columns have one weight scale.
+// The product.  Per scale block of the summed index one warp issues four M = 128,
+// N = 256, K = 32 MMAs into a fresh partial (one of two in TMEM) and one commit,
+// which frees the stage and publishes the partial through the same barrier; the
+// epilogue warps take each partial out of TMEM and add it, scaled, to FP32
+// accumulators in registers while the next block's MMAs run.
 //
-// Measured, one pair per two SMs: four such MMAs take 512 cycles (the nominal
-// rate), and a commit to both CTAs 70 to 90 of its issuer's time, so a block has
-// one commit, which frees the stage and publishes the partial through the same
-// barrier.
+// Sixteen epilogue warps of 64 accumulators take a 128 x 256 partial out in ~280
+// cycles (2 x 32-column loads each; 480 with spilled registers), below the 512 of
+// its MMAs.  What is left of a block's time is the way round: commit, wait, the
+// TMEM loads, the arrival, the next issue (with both TMEM halves in use ~880
+// cycles per block).  On CTA pairs (M = 256, the operands' shared-memory traffic
+// a third less) the longer way round through the other CTA's barriers took what
+// the rate gave: 187 us for 8192 x 4096 x 6144 both ways, and ragged groups lost
+// to the 256-row tiles (290 against 275 us); so one CTA per tile.
 // ---------------------------------------------------------------------------
 template <Mode MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
-    k_product_pair(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+__global__ void __launch_bounds__(THREADS, 1)
+    k_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ Fp8ProductArgs a) {
     extern __shared__ uint8_t smem_raw[];
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
     using SL = ScaleLayout<MODE>;
     Smem sm;
     sm.stages = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -462,7 +286,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             mbar_init(&b->full[s], 2);
             mbar_init(&b->done[s], 1);
         }
-        for (int i = 0; i < NPART; ++i) mbar_init(&b->pempty[i], 2 * EPI_WARPS);
+        for (int i = 0; i < NPART; ++i) mbar_init(&b->pempty[i], EPI_WARPS);
         for (int i = 0; i < SC_BUFS; ++i) {
             mbar_init(&b->sfull[i], 32);
             mbar_init(&b->sempty[i], EPI_WARPS);
@@ -471,19 +295,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         fence_barrier_init();
     }
     pdl_wait();  // the operands come from the previous kernels
-    if (warp == 0) build_group_table(sm.tt, a.offsets, a.G, a.M, MODE == kWeight ? BK : PM);
+    if (warp == 0) build_group_table(sm.tt, a.offsets, a.G, a.M, MODE == kWeight ? BK : BM);
     // the status word: a wait that runs out does so seconds after this store
     if (blockIdx.x == 0 && threadIdx.x == 32) *a.status = MOE_OK;
     __syncthreads();
     pdl_trigger();
-    cluster_sync();  // both CTAs' barriers exist before either signals the other
-    if (warp == MMA_WARP) tmem_alloc_pair(&b->tmem_slot, TMEM_COLS);
+    if (warp == MMA_WARP) tmem_alloc(&b->tmem_slot, TMEM_COLS);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = b->tmem_slot;
     const Work<MODE> work(a, sm.tt);
-    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
     if (warp >= EPI_WARPS) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_HELP));
@@ -492,28 +314,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             const bool is_a = warp == A_WARP;
             const CUtensorMap* map = is_a ? &tm_a : &tm_b;
             if (elect_one()) tma_prefetch_desc(map);
-            const uint32_t full_leader = in_leader(sm.full(0));
-            const uint32_t bytes = 2 * (is_a ? A_BYTES : B_BYTES);  // both CTAs'
             const uint32_t dst0 = sm.stages + (is_a ? 0 : A_BYTES);
             Ring<STAGES> st;
             uint32_t issued = 0;
             bool ok = true;
-            for (int i = pair; ok && i < work.total; i += npairs) {
-                const PTile t = work.tile(a, sm.tt, i, rank);
-                const int col = t.col0 + (int)rank * (BN / 2);
+            for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
+                const PTile t = work.tile(a, sm.tt, i);
                 int x, y;  // of the tile's first block
                 if (is_a) {
                     x = t.block0 * BK;
                     y = t.row0;
                 } else if (MODE == kForward) {
                     x = 0;
-                    y = t.g * a.N + col;
+                    y = t.g * a.N + t.col0;
                 } else if (MODE == kInput) {
-                    x = col;
+                    x = t.col0;
                     y = t.g * a.N;
                 } else {
                     x = t.block0 * BK;
-                    y = col;
+                    y = t.col0;
                 }
                 for (int kb = 0; kb < t.blocks; ++kb, st.next()) {
                     if (!warp_wait_phase(sm.done(st.slot), st.round ^ 1u, a.timeout_ns, sm.abort_flag())) {
@@ -521,12 +340,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                         break;
                     }
                     if (elect_one()) {
-                        if (rank == 0)
-                            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
-                                             sm.full(st.slot)),
-                                         "r"(bytes)
-                                         : "memory");
-                        load_pair(dst0 + st.slot * STAGE_BYTES, map, full_leader + 8 * st.slot, x, y);
+                        const uint32_t dst = dst0 + st.slot * STAGE_BYTES;
+                        expect_bytes(sm.full(st.slot), is_a ? A_BYTES : B_BYTES);
+                        tma_load(dst, map, sm.full(st.slot), x, y);
+                        if (MODE == kInput && !is_a)  // rows of 128 columns: two boxes
+                            tma_load(dst + B_BYTES / 2, map, sm.full(st.slot), x + 128, y);
                     }
                     __syncwarp();
                     ++issued;
@@ -534,45 +352,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 }
             }
             if (!ok && lane == 0) fail(sm, a.status);
-            // after a failure the pair's copies in flight are waited for (bounded)
-            if (rank == 0 && lane == 0 && *reinterpret_cast<volatile int*>(&b->abort_flag))
+            // after a failure the copies in flight are waited for (bounded)
+            if (lane == 0 && *reinterpret_cast<volatile int*>(&b->abort_flag))
                 for (uint32_t j = issued > STAGES ? issued - STAGES : 0; j < issued; ++j)
                     mbar_wait(&b->full[j % STAGES], (j / STAGES) & 1, a.timeout_ns, nullptr);
         } else if (warp == MMA_WARP) {
-            // ------------------------------------------------ MMA issuer (leader)
-            if (rank == 0) {
-                constexpr uint32_t idesc = idesc_e4m3(PM, BN) | (MODE == kInput ? kBTransposed : 0u);
-                Ring<STAGES> st;
-                Ring<NPART> pt;
-                bool ok = true;
-                for (int i = pair; ok && i < work.total; i += npairs) {
-                    const int blocks = work.tile(a, sm.tt, i, 0).blocks;
-                    for (int kb = 0; kb < blocks; ++kb, st.next(), pt.next()) {
-                        if (!warp_wait_phase(sm.full(st.slot), st.round, a.timeout_ns, sm.abort_flag()) ||
-                            !warp_wait_phase(sm.pempty(pt.slot), pt.round ^ 1u, a.timeout_ns,
-                                             sm.abort_flag())) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after_sync();
-                        const uint32_t sa = sm.stages + st.slot * STAGE_BYTES, sb = sa + A_BYTES;
-                        if (elect_one()) {
-#pragma unroll
-                            for (int kk = 0; kk < BK / 32; ++kk)
-                                // a K step: 32 bytes on (K innermost), or 32 rows on (kInput)
-                                umma_e4m3_pair(tmem + pt.slot * BN, sdesc_k_sw128(sa + kk * 32),
-                                               sdesc_k_sw128(sb + (MODE == kInput ? kk * 32 * 128 : kk * 32)),
-                                               idesc, kk != 0);
-                            commit_pair(sm.done(st.slot));
-                        }
-                        __syncwarp();
+            // ------------------------------------------------ MMA issuer
+            constexpr uint32_t idesc = idesc_e4m3(BM, BN) | (MODE == kInput ? kBTransposed : 0u);
+            Ring<STAGES> st;
+            Ring<NPART> pt;
+            bool ok = true;
+            for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
+                const int blocks = work.tile(a, sm.tt, i).blocks;
+                for (int kb = 0; kb < blocks; ++kb, st.next(), pt.next()) {
+                    if (!warp_wait_phase(sm.full(st.slot), st.round, a.timeout_ns, sm.abort_flag()) ||
+                        !warp_wait_phase(sm.pempty(pt.slot), pt.round ^ 1u, a.timeout_ns,
+                                         sm.abort_flag())) {
+                        ok = false;
+                        break;
                     }
+                    tc_fence_after_sync();
+                    const uint32_t sa = sm.stages + st.slot * STAGE_BYTES, sb = sa + A_BYTES;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < BK / 32; ++kk)
+                            // a K step: 32 bytes on (K innermost), or 32 rows on (kInput's B)
+                            umma_e4m3(tmem + pt.slot * BN, sdesc_k_sw128(sa + kk * 32),
+                                      MODE == kInput ? sdesc_mn_sw128(sb + kk * 32 * 128, B_BYTES / 2)
+                                                     : sdesc_k_sw128(sb + kk * 32),
+                                      idesc, kk != 0);
+                        mma_commit(sm.done(st.slot));
+                    }
+                    __syncwarp();
                 }
-                if (!ok && lane == 0) fail(sm, a.status);
             }
+            if (!ok && lane == 0) fail(sm, a.status);
         } else {
             // ------------------------------------------------ scales, SC_KB blocks at a time
-            scale_role<MODE>(a, sm, work, rank, pair, npairs);
+            scale_role<MODE>(a, sm, work);
         }
         __syncwarp();
     } else {
@@ -581,15 +398,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int quad = warp & 3, part = warp >> 2;  // TMEM lanes, columns
         const int row = quad * 32 + lane;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * EPI_COLS;
-        const uint32_t pempty_leader = in_leader(sm.pempty(0));
         constexpr bool CS = MODE == kWeight;
         constexpr int NQ = EPI_COLS / 32;
         Ring<STAGES> st;
         Ring<SC_BUFS> ch;
         uint32_t pb = 0;
         bool ok = true;
-        for (int i = pair; ok && i < work.total; i += npairs) {
-            const int blocks = work.tile(a, sm.tt, i, rank).blocks;
+        for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
+            const int blocks = work.tile(a, sm.tt, i).blocks;
             uint64_t acc[16 * NQ];
 #pragma unroll
             for (int j = 0; j < 16 * NQ; ++j) acc[j] = 0ull;
@@ -617,7 +433,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     tmem_arrived(r);
                     if (q == NQ - 1) {  // the partial is in registers
                         tc_fence_before_sync();
-                        warp_arrive_leader(pempty_leader + 8 * pb);
+                        __syncwarp();
+                        if (elect_one()) arrive(sm.pempty(pb));
                     }
                     promote32<CS>(r, ff, cs + 128 * q, acc + 16 * q);
                 }
@@ -634,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 break;
             }
             // decoded again rather than kept: the loop has no registers to spare
-            const PTile t = work.tile(a, sm.tt, i, rank);
+            const PTile t = work.tile(a, sm.tt, i);
             const int cols = MODE == kForward ? a.N : a.K;
             const int col = t.col0 + part * EPI_COLS;
             if (row < t.nrows && col < cols && !(MODE == kWeight && a.accumulate && t.blocks == 0)) {
@@ -647,10 +464,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     }
     tc_fence_before_sync();
     __syncthreads();
-    cluster_sync();  // neither CTA leaves while the other may still touch it
     if (warp == MMA_WARP) {
         tc_fence_after_sync();
-        tmem_dealloc_pair(tmem, TMEM_COLS);
+        tmem_dealloc(tmem, TMEM_COLS);
     }
 }
 
@@ -660,41 +476,41 @@ cudaError_t set_up_once() {
     const int dev = current_device_info().device;
     if (dev < 64 && done[dev]) return cudaSuccess;
     cudaFuncAttributes at;
-    cudaError_t e = cudaFuncGetAttributes(&at, k_product_pair<MODE>);
+    cudaError_t e = cudaFuncGetAttributes(&at, k_product<MODE>);
     if (e != cudaSuccess) return e;
     if (at.numRegs != REGS) return cudaErrorInvalidConfiguration;  // the split would not add up
-    e = cudaFuncSetAttribute(k_product_pair<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(k_product<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem_bytes<MODE>());
     if (e == cudaSuccess && dev < 64) done[dev] = true;
     return e;
 }
 
 template <Mode MODE>
-cudaError_t launch_pair(const Fp8ProductArgs& a, cudaStream_t s) {
+cudaError_t launch_tiles(const Fp8ProductArgs& a, cudaStream_t s) {
     CUtensorMap ta, tb;
     bool ok;
     int64_t tiles;
     if (MODE == kForward) {
         ok = make_tmap_2d(&ta, a.a, 1, a.M, a.K, BM, BK) &&
-             make_tmap_2d(&tb, a.b, 1, (uint64_t)a.G * a.N, a.K, BN / 2, BK);
+             make_tmap_2d(&tb, a.b, 1, (uint64_t)a.G * a.N, a.K, BN, BK);
     } else if (MODE == kInput) {
         ok = make_tmap_2d(&ta, a.a, 1, a.M, a.N, BM, BK) &&
-             make_tmap_2d(&tb, a.b, 1, (uint64_t)a.G * a.N, a.K, BK, BN / 2);
+             make_tmap_2d(&tb, a.b, 1, (uint64_t)a.G * a.N, a.K, BK, 128);
     } else {
         ok = make_tmap_2d(&ta, a.a, 1, a.N, a.rows_t, BM, BK) &&
-             make_tmap_2d(&tb, a.b, 1, a.K, a.rows_t, BN / 2, BK);
+             make_tmap_2d(&tb, a.b, 1, a.K, a.rows_t, BN, BK);
     }
     if (!ok) return cudaErrorInvalidValue;
     if (MODE == kWeight)
-        tiles = (int64_t)a.G * ((a.N + PM - 1) / PM) * ((a.K + BN - 1) / BN);
+        tiles = (int64_t)a.G * (a.N / BM) * ((a.K + BN - 1) / BN);
     else  // the groups' rows are known on the device only: at most this many
-        tiles = ((int64_t)a.M / PM + (a.G < a.M ? a.G : a.M)) *
+        tiles = ((int64_t)a.M / BM + (a.G < a.M ? a.G : a.M)) *
                 (((MODE == kForward ? a.N : a.K) + BN - 1) / BN);
     if (tiles >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
     cudaError_t e = set_up_once<MODE>();
     if (e != cudaSuccess) return e;
-    const int64_t pairs = current_device_info().num_sms / 2;
-    e = launch_pdl(k_product_pair<MODE>, dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs)),
+    const int64_t sms = current_device_info().num_sms;
+    e = launch_pdl(k_product<MODE>, dim3((unsigned)(tiles < sms ? tiles : sms)),
                    dim3(THREADS), smem_bytes<MODE>(), s, ta, tb, a);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -791,15 +607,15 @@ cudaError_t launch_quant_tokens(const uint16_t* x, const int32_t* offsets, int G
 }
 
 cudaError_t launch_gemm_fp8(const Fp8ProductArgs& a, cudaStream_t s) {
-    return launch_pair<kForward>(a, s);
+    return launch_tiles<kForward>(a, s);
 }
 
 cudaError_t launch_gemm_fp8_dgrad(const Fp8ProductArgs& a, cudaStream_t s) {
-    return launch_pair<kInput>(a, s);
+    return launch_tiles<kInput>(a, s);
 }
 
 cudaError_t launch_gemm_fp8_wgrad(const Fp8ProductArgs& a, cudaStream_t s) {
-    return launch_pair<kWeight>(a, s);
+    return launch_tiles<kWeight>(a, s);
 }
 
 }  // namespace moe

@@ -217,37 +217,56 @@ __device__ __forceinline__ void promote32(const uint32_t* r, uint64_t ff, uint32
     }
 }
 
-// Writes 32 consecutive values of one row (16-byte aligned).
+// Writes 32 consecutive values of one row.  32-byte stores where the output is
+// aligned for them (each fills a sector; a warp's 32 rows cost one pass of the
+// store unit per 32 bytes of a row instead of per 16), else 16-byte ones.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+template <int WORDS>
+__device__ __forceinline__ void store_words(uint32_t* dst, const uint32_t* v) {
+    if ((reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+#pragma unroll
+        for (int q = 0; q < WORDS; q += 8) st_global_v8(dst + q, v + q);
+    } else {
+#pragma unroll
+        for (int q = 0; q < WORDS; q += 4) st_global_v4(dst + q, v[q], v[q + 1], v[q + 2], v[q + 3]);
+    }
+}
+
 template <Mode MODE>
 __device__ __forceinline__ void store32(const Fp8ProductArgs& a, int64_t at, const uint64_t* acc) {
-    float v[32];
+    uint32_t w[32];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f32x2_unpack(acc[i], v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 16; ++i) {
+        float lo, hi;
+        f32x2_unpack(acc[i], lo, hi);
+        w[2 * i] = __float_as_uint(lo);
+        w[2 * i + 1] = __float_as_uint(hi);
+    }
     if (MODE == kWeight || a.out_type == MOE_OUT_F32) {
         float* dst = static_cast<float*>(a.out) + at;
         if (MODE == kWeight && a.accumulate) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const float4 o = *reinterpret_cast<const float4*>(dst + 4 * q);
-                v[4 * q] += o.x;
-                v[4 * q + 1] += o.y;
-                v[4 * q + 2] += o.z;
-                v[4 * q + 3] += o.w;
+                w[4 * q] = __float_as_uint(__uint_as_float(w[4 * q]) + o.x);
+                w[4 * q + 1] = __float_as_uint(__uint_as_float(w[4 * q + 1]) + o.y);
+                w[4 * q + 2] = __float_as_uint(__uint_as_float(w[4 * q + 2]) + o.z);
+                w[4 * q + 3] = __float_as_uint(__uint_as_float(w[4 * q + 3]) + o.w);
             }
         }
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<float4*>(dst + 4 * q) =
-                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-    } else if (a.out_type == MOE_OUT_F16) {
-        st_f16x32(static_cast<__half*>(a.out) + at, v);
+        store_words<32>(reinterpret_cast<uint32_t*>(dst), w);
     } else {
-        uint16_t* dst = static_cast<uint16_t*>(a.out) + at;
+        const bool f16 = a.out_type == MOE_OUT_F16;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            st_global_v4(dst + 8 * q, pack_bf16x2(v[8 * q], v[8 * q + 1]),
-                         pack_bf16x2(v[8 * q + 2], v[8 * q + 3]), pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
-                         pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+        for (int i = 0; i < 16; ++i) {
+            const float lo = __uint_as_float(w[2 * i]), hi = __uint_as_float(w[2 * i + 1]);
+            w[i] = f16 ? pack_f16x2_sat(lo, hi) : pack_bf16x2(lo, hi);
+        }
+        store_words<16>(reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at), w);
     }
 }
 
@@ -580,11 +599,8 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float s = red[0][c8 + j];
-        const __nv_fp8x2_storage_t lo = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(f[0][j], s), __fdiv_rn(f[1][j], s)), __NV_SATFINITE, __NV_E4M3);
-        const __nv_fp8x2_storage_t hi = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(f[2][j], s), __fdiv_rn(f[3][j], s)), __NV_SATFINITE, __NV_E4M3);
-        codes[c8 + j][tid >> 3] = (uint32_t)lo | ((uint32_t)hi << 16);
+        const GroupQuotient q8(s);
+        codes[c8 + j][tid >> 3] = q8.quad(f[0][j], f[1][j], f[2][j], f[3][j]);
     }
     __syncthreads();
 #pragma unroll

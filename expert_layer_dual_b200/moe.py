@@ -425,24 +425,34 @@ _OUT_TYPES = {torch.bfloat16: OUT_BF16, torch.uint16: OUT_BF16, torch.float16: O
               torch.float32: OUT_F32}
 
 
-def _want(name, t, shape, dtypes, like=None):
-    """Refuses a tensor whose shape, type or device is not the call's."""
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype not in dtypes:
-        raise ValueError(f"{name}: type {t.dtype} is not accepted")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors on {like.device}")
+def _arg(name, t, shape, dtypes, dev):
+    """Device address of a tensor of the call; refuses one whose shape, type,
+    layout or device is not the call's."""
+    if t.shape != shape or t.dtype not in dtypes or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, contiguous: "
+                         f"{t.is_contiguous()}; expected {tuple(shape)} {' or '.join(map(str, dtypes))} "
+                         f"on cuda:{dev}, contiguous")
+    return t.data_ptr()
 
 
 def _launch_device(t):
-    """The library launches on the current device: its tensors have to be there."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    """The index of the current device, on which the library launches: the
+    call's tensors have to be there."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {t.device}, not on the current CUDA device")
+    return dev
+
+
+def _ws(ws, dev):
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("workspace: not a contiguous tensor on the current CUDA device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 _F32, _I32 = (torch.float32,), (torch.int32,)
 _CODES = (torch.uint8, torch.float8_e4m3fn)
+_BF16 = (torch.bfloat16, torch.uint16)
 _MASK = (torch.uint8, torch.bool)
 
 
@@ -453,20 +463,15 @@ def balance_workspace_bytes(T: int, E: int) -> int:
 def balance_loss(logits, ids, mask, coef, loss, counts, prob_mean, tokens, ws, stream=None):
     """moe_balance_loss: loss [1], counts [E], prob_mean [E] and tokens [1] of
     logits [T, E] and the selected ids [T, k]; mask [T] (uint8 or bool) or None."""
+    dev = _launch_device(logits)
     T, E = logits.shape
     k = ids.shape[1]
-    _launch_device(logits)
-    _want("logits", logits, (T, E), _F32)
-    _want("ids", ids, (T, k), _I32, logits)
-    if mask is not None:
-        _want("mask", mask, (T,), _MASK, logits)
-    _want("loss", loss, (1,), _F32, logits)
-    _want("counts", counts, (E,), _I32, logits)
-    _want("prob_mean", prob_mean, (E,), _F32, logits)
-    _want("tokens", tokens, (1,), _I32, logits)
-    _check(_lib.moe_balance_loss(_p(logits), _p(ids), _p(mask), T, E, k, float(coef), _p(loss),
-                                 _p(counts), _p(prob_mean), _p(tokens), _p(ws),
-                                 ws.numel() * ws.element_size(), _stream(stream)), "moe_balance_loss")
+    _check(_lib.moe_balance_loss(
+        _arg("logits", logits, (T, E), _F32, dev), _arg("ids", ids, (T, k), _I32, dev),
+        None if mask is None else _arg("mask", mask, (T,), _MASK, dev), T, E, k, coef,
+        _arg("loss", loss, (1,), _F32, dev), _arg("counts", counts, (E,), _I32, dev),
+        _arg("prob_mean", prob_mean, (E,), _F32, dev), _arg("tokens", tokens, (1,), _I32, dev),
+        *_ws(ws, dev), _stream(stream)), "moe_balance_loss")
 
 
 def route_backward(logits, ids, w, dw, mask, renormalize, dloss, coef, counts, tokens, dlogits,
@@ -475,46 +480,40 @@ def route_backward(logits, ids, w, dw, mask, renormalize, dloss, coef, counts, t
     top-k weights w (None: without that part) and dloss [1] of the balance loss
     (None: without it); w may be None without dw, counts and tokens without
     dloss."""
+    dev = _launch_device(logits)
     T, E = logits.shape
     k = ids.shape[1]
-    _launch_device(logits)
-    _want("logits", logits, (T, E), _F32)
-    _want("ids", ids, (T, k), _I32, logits)
-    if dw is not None:
-        _want("dw", dw, (T, k), _F32, logits)
-        _want("w", w, (T, k), _F32, logits)
-    if mask is not None:
-        _want("mask", mask, (T,), _MASK, logits)
-    if dloss is not None:
-        _want("dloss", dloss, (1,), _F32, logits)
-        _want("counts", counts, (E,), _I32, logits)
-        _want("tokens", tokens, (1,), _I32, logits)
-    _want("dlogits", dlogits, (T, E), _F32, logits)
-    _check(_lib.moe_route_backward(_p(logits), _p(ids), _p(w), _p(dw), _p(mask), T, E, k,
-                                   int(bool(renormalize)), _p(dloss), float(coef), _p(counts),
-                                   _p(tokens), _p(dlogits), _stream(stream)), "moe_route_backward")
+    a = (_arg("logits", logits, (T, E), _F32, dev), _arg("ids", ids, (T, k), _I32, dev))
+    parts = (None, None) if dw is None else (_arg("w", w, (T, k), _F32, dev),
+                                             _arg("dw", dw, (T, k), _F32, dev))
+    aux = (None, None, None) if dloss is None else (_arg("dloss", dloss, (1,), _F32, dev),
+                                                    _arg("counts", counts, (E,), _I32, dev),
+                                                    _arg("tokens", tokens, (1,), _I32, dev))
+    _check(_lib.moe_route_backward(
+        *a, *parts, None if mask is None else _arg("mask", mask, (T,), _MASK, dev), T, E, k,
+        1 if renormalize else 0, aux[0], coef, aux[1], aux[2],
+        _arg("dlogits", dlogits, (T, E), _F32, dev), _stream(stream)), "moe_route_backward")
 
 
 def _weight_shape(w_q, offsets):
     """(G, N, K) of weight codes [N, K] or [G, N, K]."""
-    G, (N, K) = (w_q.shape[0] if w_q.dim() == 3 else 1), w_q.shape[-2:]
+    shape = w_q.shape
+    G = shape[0] if len(shape) == 3 else 1
     if offsets is None and G != 1:
         raise ValueError("several weight matrices need offsets")
-    return G, N, K
+    return G, shape[-2], shape[-1]
 
 
 def _product(entry, name, a_q, a_s, w_q, w_s, offsets, out, a_cols, out_cols, G, N, K, ws, stream):
+    dev = _launch_device(a_q)
     M = a_q.shape[0]
-    _launch_device(a_q)
-    _want("codes", a_q, (M, a_cols), _CODES)
-    _want("scales", a_s, (M, a_cols // 128), _F32, a_q)
-    _want("weight codes", w_q, w_q.shape, _CODES, a_q)
-    _want("weight scales", w_s, tuple(w_q.shape[:-2]) + (N // 128, K // 128), _F32, a_q)
-    if offsets is not None:
-        _want("offsets", offsets, (G + 1,), _I32, a_q)
-    _want("output", out, (M, out_cols), _OUT_TYPES, a_q)
-    _check(entry(_p(a_q), _p(a_s), _p(w_q), _p(w_s), _p(offsets), G, M, N, K, _p(out),
-                 _OUT_TYPES[out.dtype], _p(ws), ws.numel() * ws.element_size(), _stream(stream)), name)
+    _check(entry(
+        _arg("codes", a_q, (M, a_cols), _CODES, dev), _arg("scales", a_s, (M, a_cols // 128), _F32, dev),
+        _arg("weight codes", w_q, w_q.shape, _CODES, dev),
+        _arg("weight scales", w_s, w_q.shape[:-2] + (N // 128, K // 128), _F32, dev),
+        None if offsets is None else _arg("offsets", offsets, (G + 1,), _I32, dev), G, M, N, K,
+        _arg("output", out, (M, out_cols), _OUT_TYPES, dev), _OUT_TYPES[out.dtype], *_ws(ws, dev),
+        _stream(stream)), name)
 
 
 def gemm_fp8(x_q, x_s, w_q, w_s, offsets, y, ws, stream=None):
@@ -541,35 +540,28 @@ def fp8_token_rows(M: int, G: int = 1) -> int:
 def quantize_fp8_tokens(x, offsets, q_t, scale_t, stream=None):
     """moe_quantize_fp8_tokens: x [M, cols] (bf16) -> q_t [cols, R] e4m3 codes,
     scale_t [R/128, cols], R = fp8_token_rows(M, G)."""
+    dev = _launch_device(x)
     M, cols = x.shape
-    G = 1 if offsets is None else offsets.numel() - 1
-    R = fp8_token_rows(M, G)
-    _launch_device(x)
-    _want("x", x, (M, cols), (torch.bfloat16, torch.uint16))
-    if offsets is not None:
-        _want("offsets", offsets, (G + 1,), _I32, x)
-    _want("codes", q_t, (cols, R), _CODES, x)
-    _want("scales", scale_t, (R // 128, cols), _F32, x)
-    _check(_lib.moe_quantize_fp8_tokens(_p(x), _p(offsets), G, M, cols, _p(q_t), _p(scale_t),
-                                        _stream(stream)), "moe_quantize_fp8_tokens")
+    G = 1 if offsets is None else offsets.shape[0] - 1
+    R = _lib.moe_fp8_token_rows(M, G)
+    _check(_lib.moe_quantize_fp8_tokens(
+        _arg("x", x, (M, cols), _BF16, dev),
+        None if offsets is None else _arg("offsets", offsets, (G + 1,), _I32, dev), G, M, cols,
+        _arg("codes", q_t, (cols, R), _CODES, dev), _arg("scales", scale_t, (R // 128, cols), _F32, dev),
+        _stream(stream)), "moe_quantize_fp8_tokens")
 
 
 def gemm_fp8_wgrad(dy_t, dy_ts, x_t, x_ts, offsets, M, dw, accumulate, ws, stream=None):
     """moe_gemm_fp8_wgrad: dw [N, K] or [G, N, K] (f32) = (or +=, accumulate)
     dy^T x over each group's rows, from quantize_fp8_tokens' outputs."""
+    dev = _launch_device(dw)
     G, N, K = _weight_shape(dw, offsets)
-    R = fp8_token_rows(M, G)
-    _launch_device(dw)
-    _want("dw", dw, dw.shape, _F32)
-    _want("dy codes", dy_t, (N, R), _CODES, dw)
-    _want("dy scales", dy_ts, (R // 128, N), _F32, dw)
-    _want("x codes", x_t, (K, R), _CODES, dw)
-    _want("x scales", x_ts, (R // 128, K), _F32, dw)
-    if offsets is not None:
-        _want("offsets", offsets, (G + 1,), _I32, dw)
-    _check(_lib.moe_gemm_fp8_wgrad(_p(dy_t), _p(dy_ts), _p(x_t), _p(x_ts), _p(offsets), G, M, N, K,
-                                   _p(dw), int(bool(accumulate)), _p(ws),
-                                   ws.numel() * ws.element_size(), _stream(stream)),
+    R = _lib.moe_fp8_token_rows(M, G)
+    _check(_lib.moe_gemm_fp8_wgrad(
+        _arg("dy codes", dy_t, (N, R), _CODES, dev), _arg("dy scales", dy_ts, (R // 128, N), _F32, dev),
+        _arg("x codes", x_t, (K, R), _CODES, dev), _arg("x scales", x_ts, (R // 128, K), _F32, dev),
+        None if offsets is None else _arg("offsets", offsets, (G + 1,), _I32, dev), G, M, N, K,
+        _arg("dw", dw, dw.shape, _F32, dev), 1 if accumulate else 0, *_ws(ws, dev), _stream(stream)),
            "moe_gemm_fp8_wgrad")
 
 

@@ -344,3 +344,35 @@ def test_training_step_of_routed_experts():
     lhs = float((ref.rows64(dq.cpu(), ds.cpu()) * yw).sum())
     rhs = float((dxw * ref.rows64(xq.cpu(), xs.cpu())).sum())
     assert abs(lhs - rhs) <= 1e-9 * float((dxw.abs() * ref.rows64(xq.cpu(), xs.cpu()).abs()).sum())
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -60, 2.0 ** 60, 2.0 ** -115, 2.0 ** 118, 3.0e-39])
+def test_codes_of_every_bf16_value(scale):
+    """Every finite bf16 pattern, scaled into a group whose largest magnitude is
+    448 * scale or the pattern's own: the codes of both quantisers are the
+    rounded FP32 quotients (ties, e4m3 subnormals and saturation among them)."""
+    bits = torch.arange(0, 65536, dtype=torch.int32).to(torch.int16)
+    v = bits.view(torch.bfloat16)
+    v = v[torch.isfinite(v)].float()
+    v = (v * scale).to(torch.bfloat16)
+    v = v[torch.isfinite(v)]
+    v = v[v.abs().float() <= 448.0 * scale] if scale >= 1.0 else v
+    tops = torch.tensor([448.0, 1.0, 3.7, 100.0, 2.0 ** -7]) * scale
+    rows = []
+    for top in tops.tolist():
+        w = v[v.abs().float() <= top]
+        w = w[: w.numel() // 127 * 127].reshape(-1, 127)
+        rows.append(torch.cat([torch.full((w.shape[0], 1), top).to(torch.bfloat16), w], 1))
+    x = torch.cat(rows)                                   # groups of 128, the first value the largest
+    q = torch.empty(x.shape, dtype=torch.uint8, device=DEV)
+    s = torch.empty((x.shape[0], 1), device=DEV)
+    M.quantize_act_fp8(x.to(DEV), q, s)
+    wq, ws = ref.quantise_rows(x)
+    assert torch.equal(s.cpu(), ws) and torch.equal(q.cpu(), wq)
+    xt = x[: x.shape[0] // 128 * 128].T.contiguous()      # the same groups along the tokens
+    R = M.fp8_token_rows(128, 1)
+    qt = torch.empty((xt.shape[1], R), dtype=torch.uint8, device=DEV)
+    st = torch.empty((1, xt.shape[1]), device=DEV)
+    M.quantize_fp8_tokens(xt.to(DEV), None, qt, st)
+    n = xt.shape[1]
+    assert torch.equal(qt.cpu(), wq[:n]) and torch.equal(st.cpu()[0], ws[:n, 0])

@@ -541,8 +541,8 @@ cudaError_t launch_tiles(const Fp8ProductArgs& a, cudaStream_t s) {
 // and the weight gradient reads both operands along the tokens.  A block of
 // threads takes 128 tokens x 64 columns: 16-byte loads, the column maxima by
 // shuffles and shared memory, and the codes turned in shared memory so that
-// each column's 128 codes leave as one 128-byte run.  Bound by HBM: 2 bytes
-// read and 1 written per value.
+// each column's 128 codes leave as one 128-byte run.  2 bytes are read and 1
+// written per value.
 // ---------------------------------------------------------------------------
 constexpr int QC = 64;
 
@@ -550,7 +550,8 @@ __global__ void __launch_bounds__(256)
     k_quant_tokens(const uint16_t* __restrict__ x, const int32_t* __restrict__ offsets, int G, int M,
                    int cols, int64_t rows_t, uint8_t* __restrict__ q, float* __restrict__ scale) {
     __shared__ TileTable tt;
-    __shared__ float red[8][QC];
+    __shared__ uint32_t red[8][QC / 2];
+    __shared__ float2 quot[QC];
     __shared__ uint32_t codes[QC][33];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
@@ -562,45 +563,49 @@ __global__ void __launch_bounds__(256)
     const int g = group_of(&tt, G, blk);
     const int64_t row0 = tt.goff[g] + (int64_t)(blk - tt.mstart[g]) * 128;
     const int rows = min((int64_t)128, tt.goff[g + 1] - row0);
+    // a thread: four tokens of eight columns, a word holding two columns
     const int c0 = blockIdx.x * QC, c8 = (tid & 7) * 8, r4 = (tid >> 3) * 4;
-    float f[4][8], m[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m[j] = 0.0f;
+    uint32_t w[4][4], m[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint4 u = make_uint4(0, 0, 0, 0);
         if (r4 + i < rows)
             u = __ldg(reinterpret_cast<const uint4*>(x + (row0 + r4 + i) * cols + c0 + c8));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            f[i][2 * j] = __uint_as_float(w[j] << 16);
-            f[i][2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = fmaxf(m[j], fabsf(f[i][j]));
+        w[i][0] = u.x;
+        w[i][1] = u.y;
+        w[i][2] = u.z;
+        w[i][3] = u.w;
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 8));
-        m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
-        if (lane < 8) red[warp][c8 + j] = m[j];
+    for (int j = 0; j < 4; ++j) {
+        m[j] = bf16x2_absmax4(w[0][j], w[1][j], w[2][j], w[3][j]);
+        m[j] = bf16x2_max(m[j], __shfl_xor_sync(0xffffffffu, m[j], 8));
+        m[j] = bf16x2_max(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
     }
+    if (lane < 8) *reinterpret_cast<uint4*>(&red[warp][c8 / 2]) = make_uint4(m[0], m[1], m[2], m[3]);
     __syncthreads();
     if (tid < QC) {
-        float a = red[0][tid];
+        uint32_t a = red[0][tid / 2];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) a = fmaxf(a, red[w][tid]);
-        const float s = a == 0.0f ? 1.0f : __fdiv_rn(a, 448.0f);
-        scale[(int64_t)blk * cols + c0 + tid] = s;
-        red[0][tid] = s;
+        for (int v = 1; v < 8; ++v) a = bf16x2_max(a, red[v][tid / 2]);
+        const GroupQuotient q8(block_scale(__uint_as_float((tid & 1) ? a & 0xFFFF0000u : a << 16)));
+        scale[(int64_t)blk * cols + c0 + tid] = q8.s;
+        quot[tid] = make_float2(q8.s, q8.r);
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float s = red[0][c8 + j];
-        const GroupQuotient q8(s);
-        codes[c8 + j][tid >> 3] = q8.quad(f[0][j], f[1][j], f[2][j], f[3][j]);
+    for (int j = 0; j < 4; ++j) {
+        // the two columns of word j, four tokens each: the words' low and high halves
+        const uint32_t a = w[0][j], b = w[1][j], c = w[2][j], d = w[3][j];
+        const float4 t = *reinterpret_cast<const float4*>(&quot[c8 + 2 * j]);
+        codes[c8 + 2 * j][tid >> 3] = GroupQuotient(t.x, t.y).codes4(
+            f32x2_pack(__uint_as_float(a << 16), __uint_as_float(b << 16)),
+            f32x2_pack(__uint_as_float(c << 16), __uint_as_float(d << 16)),
+            __byte_perm(__byte_perm(a, b, 0x0051), __byte_perm(c, d, 0x0051), 0x5410));
+        codes[c8 + 2 * j + 1][tid >> 3] = GroupQuotient(t.z, t.w).codes4(
+            f32x2_pack(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u)),
+            f32x2_pack(__uint_as_float(c & 0xFFFF0000u), __uint_as_float(d & 0xFFFF0000u)),
+            __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410));
     }
     __syncthreads();
 #pragma unroll

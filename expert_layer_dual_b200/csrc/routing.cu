@@ -627,18 +627,18 @@ __global__ void __launch_bounds__(256)
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float f[8];
-        bf16x8_to_f32(u[i], f);
-        float amax = 0.0f;
+        uint32_t m = bf16x2_absmax4(u[i].x, u[i].y, u[i].z, u[i].w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const GroupQuotient g(group_scale(amax));
+        for (int o = 8; o > 0; o >>= 1) m = bf16x2_max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float amax = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+        const GroupQuotient g(block_scale(amax));
         const int c = c0 + i * 256;
         if (c < cols) {
-            const uint2 o = make_uint2(g.quad(f[0], f[1], f[2], f[3]), g.quad(f[4], f[5], f[6], f[7]));
-            *reinterpret_cast<uint2*>(q + r * cols + c) = o;
+            *reinterpret_cast<uint2*>(q + r * cols + c) =
+                make_uint2(g.codes4(bf16x2_widen(u[i].x), bf16x2_widen(u[i].y),
+                                    __byte_perm(u[i].x, u[i].y, 0x7531)),
+                           g.codes4(bf16x2_widen(u[i].z), bf16x2_widen(u[i].w),
+                                    __byte_perm(u[i].z, u[i].w, 0x7531)));
             if ((lane & 15) == 0) scale[r * (cols / 128) + c / 128] = g.s;
         }
     }

@@ -376,3 +376,15 @@ def test_codes_of_every_bf16_value(scale):
     M.quantize_fp8_tokens(xt.to(DEV), None, qt, st)
     n = xt.shape[1]
     assert torch.equal(qt.cpu(), wq[:n]) and torch.equal(st.cpu()[0], ws[:n, 0])
+
+
+def test_scale_of_every_bf16_maximum():
+    """s = fp32(amax) / 448 by the IEEE division for every positive finite bf16 amax."""
+    top = torch.arange(0, 0x7F80, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = torch.zeros((top.numel(), 128), dtype=torch.bfloat16)
+    x[:, 77] = -top
+    q = torch.empty(x.shape, dtype=torch.uint8, device=DEV)
+    s = torch.empty((x.shape[0], 1), device=DEV)
+    M.quantize_act_fp8(x.to(DEV), q, s)
+    wq, ws = ref.quantise_rows(x)
+    assert torch.equal(s.cpu(), ws) and torch.equal(q.cpu(), wq)

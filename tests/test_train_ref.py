@@ -1,7 +1,9 @@
 """The 64-bit formulas of the training operators against differences, and the
 host-side refusals of their entry points (no GPU)."""
 import ctypes
+from fractions import Fraction
 
+import numpy as np
 import pytest
 import torch
 
@@ -78,6 +80,33 @@ def test_token_layout_and_adjoints():
     dw = torch.stack([dy64[a:b].T @ x64[a:b] for a, b in ((0, 130), (130, 130), (130, 200))])
     a, b, c = (dy64 * y).sum(), (dx * x64).sum(), (dw * w64).sum()
     assert abs(a - b) < 1e-9 * abs(a) + 1e-8 and abs(a - c) < 1e-9 * abs(a) + 1e-8
+
+
+def _rn(x):
+    """A positive fraction rounded to FP32 (nearest, ties to even; normal range)."""
+    f = np.float32(float(x))
+    near = [np.nextafter(f, np.float32(0)), f, np.nextafter(f, np.float32(np.inf))]
+    return min(near, key=lambda c: (abs(Fraction(float(c)) - x), int(c.view(np.uint32)) & 1))
+
+
+def test_corrected_quotient_is_the_rounded_one():
+    """The quantisers' quotient: the product with the reciprocal, corrected by one
+    FMA residual, equals fp32(v / s) for every bf16 significand v and the scale s =
+    fp32(b / 448) of every bf16 significand b, with the reciprocal one ulp off
+    either way too; and s itself comes out of the same correction."""
+    def corrected(v, r, s):
+        q = _rn(Fraction(v) * Fraction(float(r)))
+        e = Fraction(v) - Fraction(float(q)) * s
+        e32 = Fraction(float(_rn(abs(e)))) * (1 if e > 0 else -1) if e else e
+        return _rn(e32 * Fraction(float(r)) + Fraction(float(q)))
+
+    for b in range(128, 256):
+        s = _rn(Fraction(b, 448))
+        assert corrected(b, _rn(Fraction(1, 448)), Fraction(448)) == s
+        r0 = _rn(1 / Fraction(float(s)))
+        for r in (np.nextafter(r0, np.float32(0)), r0, np.nextafter(r0, np.float32(np.inf))):
+            for v in range(128, 256):
+                assert corrected(v, r, Fraction(float(s))) == _rn(Fraction(v) / Fraction(float(s)))
 
 
 # ------------------------------------------------------------------ refusals

@@ -313,15 +313,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         b->abort_flag = 0;
         fence_barrier_init();
     }
+    if (warp == MMA_WARP) tmem_alloc(&b->tmem_slot, TMEM_COLS);
     pdl_wait();  // the operands come from the previous kernels
     if (warp == 0) build_group_table(sm.tt, a.offsets, a.G, a.M, MODE == kWeight ? BK : BM);
     // the status word: a wait that runs out does so seconds after this store
     if (blockIdx.x == 0 && threadIdx.x == 32) *a.status = MOE_OK;
-    __syncthreads();
-    pdl_trigger();
-    if (warp == MMA_WARP) tmem_alloc(&b->tmem_slot, TMEM_COLS);
     tc_fence_before_sync();
     __syncthreads();
+    pdl_trigger();
     tc_fence_after_sync();
     const uint32_t tmem = b->tmem_slot;
     const Work<MODE> work(a, sm.tt);
@@ -628,11 +627,11 @@ cudaError_t launch_quant_tokens(const uint16_t* x, const int32_t* offsets, int G
 }
 
 cudaError_t launch_gemm_fp8(const Fp8ProductArgs& a, cudaStream_t s) {
-    return launch_tiles<kForward>(a, s);
+    return use_few_rows(a.M, a.G) ? launch_gemm_fp8_few(a, s) : launch_tiles<kForward>(a, s);
 }
 
 cudaError_t launch_gemm_fp8_dgrad(const Fp8ProductArgs& a, cudaStream_t s) {
-    return launch_tiles<kInput>(a, s);
+    return use_few_rows(a.M, a.G) ? launch_gemm_fp8_dgrad_few(a, s) : launch_tiles<kInput>(a, s);
 }
 
 cudaError_t launch_gemm_fp8_wgrad(const Fp8ProductArgs& a, cudaStream_t s) {

@@ -249,6 +249,11 @@ struct Fp8ProductArgs {
 cudaError_t launch_gemm_fp8(const Fp8ProductArgs& a, cudaStream_t s);
 cudaError_t launch_gemm_fp8_dgrad(const Fp8ProductArgs& a, cudaStream_t s);
 cudaError_t launch_gemm_fp8_wgrad(const Fp8ProductArgs& a, cudaStream_t s);
+// ---- gemm_fp8_few.cu (the same products for few rows per group: tiles of kFewRows rows)
+constexpr int kFewRows = 64;
+cudaError_t launch_gemm_fp8_few(const Fp8ProductArgs& a, cudaStream_t s);
+cudaError_t launch_gemm_fp8_dgrad_few(const Fp8ProductArgs& a, cudaStream_t s);
+inline bool use_few_rows(int M, int G) { return (int64_t)M <= (int64_t)kFewRows * G; }
 cudaError_t launch_quant_tokens(const uint16_t* x, const int32_t* offsets, int G, int M, int cols,
                                 uint8_t* q, float* scale, cudaStream_t s);
 

@@ -226,6 +226,21 @@ __device__ __forceinline__ void tmem_arrived(uint32_t* r) {
                  :
                  : "memory");
 }
+// The same for 16 columns.
+__device__ __forceinline__ void tmem_fetch16(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : W4(r, 0), W4(r, 4), W4(r, 8), W4(r, 12)
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_arrived16(uint32_t* r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : R4(r, 0), R4(r, 4), R4(r, 8), R4(r, 12)
+                 :
+                 : "memory");
+}
 #undef R4
 #undef W4
 

@@ -25,15 +25,15 @@ constexpr int FM = 128, FN = kFewRows, BK = 128;  // output columns and rows of 
 constexpr int STAGES = 7, A_BYTES = FM * BK, B_BYTES = FN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
 constexpr int NPART = 4;                          // partials of FN TMEM columns
 constexpr uint32_t TMEM_COLS = NPART * FN;
-constexpr int EPI_WARPS = 4, MMA_WARP = 4, A_WARP = 5, B_WARP = 6, SCALE_WARP = 7;
+constexpr int EPI_WARPS = 8, MMA_WARP = 8, A_WARP = 9, B_WARP = 10, SCALE_WARP = 11;
+constexpr int EPI_ROWS = FN * 4 / EPI_WARPS;      // rows (TMEM columns) of an epilogue warp
 constexpr int THREADS = 32 * (SCALE_WARP + 1);
 constexpr int SC_KB = 4, SC_BUFS = 4;             // scales: chunks of 4 blocks, four ahead
 constexpr int RED_FLOATS = FN * FM;               // the tile left for the cluster
 
 struct Bars {
     uint64_t full[STAGES];     // two arming arrivals (A and B) + their bytes
-    uint64_t done[STAGES];     // MMA commit: the stage is free
-    uint64_t pfull[NPART];     // MMA commit: the partial is complete
+    uint64_t done[STAGES];     // MMA commit: the stage is free, the block's partial complete
     uint64_t pempty[NPART];    // partial read (one arrival per epilogue warp)
     uint64_t sfull[SC_BUFS];   // scale chunk written
     uint64_t sempty[SC_BUFS];  // scale chunk read (one arrival per epilogue warp)
@@ -52,7 +52,6 @@ struct Smem {
     TileTable* tt;
     __device__ __forceinline__ uint32_t full(int i) const { return bars + offsetof(Bars, full) + 8 * i; }
     __device__ __forceinline__ uint32_t done(int i) const { return bars + offsetof(Bars, done) + 8 * i; }
-    __device__ __forceinline__ uint32_t pfull(int i) const { return bars + offsetof(Bars, pfull) + 8 * i; }
     __device__ __forceinline__ uint32_t pempty(int i) const { return bars + offsetof(Bars, pempty) + 8 * i; }
     __device__ __forceinline__ uint32_t sfull(int i) const { return bars + offsetof(Bars, sfull) + 8 * i; }
     __device__ __forceinline__ uint32_t sempty(int i) const { return bars + offsetof(Bars, sempty) + 8 * i; }
@@ -112,13 +111,14 @@ __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity,
     return __all_sync(0xffffffffu, ok);
 }
 
-// 16 FP32 columns of this thread's TMEM lane times their scales (16 floats at shared
-// address cs), added to acc.
-__device__ __forceinline__ void promote16(uint32_t taddr, uint32_t cs, uint64_t* acc) {
-    float v[16];
-    tmem_load16(taddr, v);
+// acc += columns (of this thread's TMEM lane) times their scales (floats at shared
+// address cs).
+template <int COLS>
+__device__ __forceinline__ void promote(uint32_t taddr, uint32_t cs, uint64_t* acc) {
+    float v[COLS];
+    if (COLS == 32) tmem_load32(taddr, v); else tmem_load16(taddr, v);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < COLS / 4; ++i) {
         const float4 s = lds4(cs + 16 * i);
         acc[2 * i] = f32x2_fma(f32x2_pack(v[4 * i], v[4 * i + 1]), f32x2_pack(s.x, s.y), acc[2 * i]);
         acc[2 * i + 1] =
@@ -133,6 +133,37 @@ __device__ __forceinline__ void store_one(void* out, int64_t at, float v, int ty
         static_cast<uint16_t*>(out)[at] = (uint16_t)pack_f16x2_sat(v, 0.0f);
     else
         static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(v);
+}
+
+// The cluster's sums of one column (at shared address `here` of every CTA) for rows
+// rank + (2j + odd) * SIZE, written to the output; four rows' loads in flight.
+template <int SIZE>
+__device__ __forceinline__ void add_rows(const Fp8ProductArgs& a, uint32_t here, int64_t at, int cols,
+                                         int nrows, uint32_t rank, int odd) {
+    uint32_t base[SIZE];
+#pragma unroll
+    for (int q = 0; q < SIZE; ++q) base[q] = in_rank(here, q);
+    constexpr int U = SIZE == 8 ? 2 : 4, STEP = 2 * SIZE;
+    for (int r = (int)rank + odd * SIZE; r < nrows; r += U * STEP) {
+        float v[U][SIZE];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int q = 0; q < SIZE; ++q)
+                if (r + u * STEP < nrows)
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(v[u][q])
+                                 : "r"(base[q] + 4u * (r + u * STEP) * FM)
+                                 : "memory");
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (r + u * STEP >= nrows) break;
+            float s = v[u][0];
+#pragma unroll
+            for (int q = 1; q < SIZE; ++q) s += v[u][q];
+            store_one(a.out, at + (int64_t)(r + u * STEP) * cols, s, a.out_type);
+        }
+    }
 }
 
 template <bool INPUT>
@@ -155,10 +186,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&b->full[s], 2);
             mbar_init(&b->done[s], 1);
         }
-        for (int i = 0; i < NPART; ++i) {
-            mbar_init(&b->pfull[i], 1);
-            mbar_init(&b->pempty[i], EPI_WARPS);
-        }
+        for (int i = 0; i < NPART; ++i) mbar_init(&b->pempty[i], EPI_WARPS);
         for (int i = 0; i < SC_BUFS; ++i) {
             mbar_init(&b->sfull[i], 1);
             mbar_init(&b->sempty[i], EPI_WARPS);
@@ -246,7 +274,6 @@ __global__ void __launch_bounds__(THREADS, 1)
                                         : sdesc_k_sw128(sa + kk * 32),
                                   sdesc_k_sw128(sb + kk * 32), idesc, kk != 0);
                     mma_commit(sm.done(st.slot));
-                    mma_commit(sm.pfull(pt.slot));
                 }
                 __syncwarp();
             }
@@ -293,32 +320,36 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!ok && lane == 0) fail(sm, a.status);
     } else {
         // ---------------------------------------------------- promotion and output
-        const int col = warp * 32 + lane;  // this thread's output column of the tile
-        const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const int quad = warp & 3, r0 = (warp >> 2) * EPI_ROWS;
+        const int col = quad * 32 + lane;  // this thread's output column of the tile; its rows r0 ..
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + r0;
         const int cols = INPUT ? a.K : a.N;
+        Ring<STAGES> st;
         Ring<NPART> pt;
         Ring<SC_BUFS> ch;
         uint32_t turn = 0;  // of the cluster's exchange
         bool ok = true;
         for (int i = first; ok && i < total; i += step) {
             const Tile t = decode_tile(sm.tt, a.G, n_tiles, i, FN);
-            uint64_t acc[FN / 2];
+            const int mine = min(EPI_ROWS, t.nrows - r0);  // rows of this warp (may be none)
+            uint64_t acc[EPI_ROWS / 2];
 #pragma unroll
-            for (int j = 0; j < FN / 2; ++j) acc[j] = 0ull;
+            for (int j = 0; j < EPI_ROWS / 2; ++j) acc[j] = 0ull;
 #pragma unroll 1
-            for (int kb = 0; kb < blocks; ++kb, pt.next()) {
+            for (int kb = 0; kb < blocks; ++kb, st.next(), pt.next()) {
                 const int kk = kb % SC_KB;
                 if ((kk == 0 &&
                      !warp_wait_phase(sm.sfull(ch.slot), ch.round, a.timeout_ns, sm.abort_flag())) ||
-                    !warp_wait_phase(sm.pfull(pt.slot), pt.round, a.timeout_ns, sm.abort_flag())) {
+                    !warp_wait_phase(sm.done(st.slot), st.round, a.timeout_ns, sm.abort_flag())) {
                     ok = false;
                     break;
                 }
                 tc_fence_after_sync();
-                const uint32_t cs = sm.scales + 4u * (ch.slot * SC_KB + kk) * FN;
-#pragma unroll
-                for (int c = 0; c < FN / 16; ++c)
-                    if (c * 16 < t.nrows) promote16(taddr + pt.slot * FN + 16 * c, cs + 64 * c, acc + 8 * c);
+                const uint32_t cs = sm.scales + 4u * ((ch.slot * SC_KB + kk) * FN + r0);
+                if (mine > 16)
+                    promote<32>(taddr + pt.slot * FN, cs, acc);
+                else if (mine > 0)
+                    promote<16>(taddr + pt.slot * FN, cs, acc);
                 tc_fence_before_sync();
                 __syncwarp();
                 if (elect_one()) arrive(sm.pempty(pt.slot));
@@ -334,12 +365,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int64_t at = (int64_t)t.row0 * cols + t.n * FM + col;
             if (size == 1) {
 #pragma unroll
-                for (int j = 0; j < FN / 2; ++j) {
+                for (int j = 0; j < EPI_ROWS / 2; ++j) {
                     float lo, hi;
                     f32x2_unpack(acc[j], lo, hi);
-                    if (2 * j < t.nrows) store_one(a.out, at + (int64_t)(2 * j) * cols, lo, a.out_type);
-                    if (2 * j + 1 < t.nrows)
-                        store_one(a.out, at + (int64_t)(2 * j + 1) * cols, hi, a.out_type);
+                    if (2 * j < mine) store_one(a.out, at + (int64_t)(r0 + 2 * j) * cols, lo, a.out_type);
+                    if (2 * j + 1 < mine)
+                        store_one(a.out, at + (int64_t)(r0 + 2 * j + 1) * cols, hi, a.out_type);
                 }
             } else {
                 // leave the tile for the cluster once its last readers are through
@@ -347,15 +378,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (lane == 0) fail(sm, a.status);
                     break;
                 }
-                const uint32_t mine = sm.red + 4u * col;
+                const uint32_t here = sm.red + 4u * col;
 #pragma unroll
-                for (int j = 0; j < FN / 2; ++j) {
+                for (int j = 0; j < EPI_ROWS / 2; ++j) {
                     float lo, hi;
                     f32x2_unpack(acc[j], lo, hi);
-                    if (2 * j < t.nrows) {
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + 4u * (2 * j) * FM), "f"(lo) : "memory");
-                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + 4u * (2 * j + 1) * FM), "f"(hi)
-                                     : "memory");
+                    if (2 * j < mine) {
+                        const uint32_t d = here + 4u * (r0 + 2 * j) * FM;
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(d), "f"(lo) : "memory");
+                        asm volatile("st.shared.f32 [%0], %1;" ::"r"(d + 4u * FM), "f"(hi) : "memory");
                     }
                 }
                 arrive_cluster(sm.rfull(), size);
@@ -363,18 +394,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (lane == 0) fail(sm, a.status);
                     break;
                 }
-#pragma unroll 2
-                for (int r = (int)rank; r < t.nrows; r += (int)size) {
-                    float s = 0.0f;
-                    for (uint32_t q = 0; q < size; ++q) {
-                        float v;
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                     : "=f"(v)
-                                     : "r"(in_rank(mine + 4u * r * FM, q))
-                                     : "memory");
-                        s += v;
-                    }
-                    store_one(a.out, at + (int64_t)r * cols, s, a.out_type);
+                // rows rank, rank + size, ..: alternately by the two warps of a column
+                switch (size) {
+                    case 2: add_rows<2>(a, here, at, cols, t.nrows, rank, warp >> 2); break;
+                    case 4: add_rows<4>(a, here, at, cols, t.nrows, rank, warp >> 2); break;
+                    default: add_rows<8>(a, here, at, cols, t.nrows, rank, warp >> 2); break;
                 }
                 arrive_cluster(sm.rempty(), size);
                 ++turn;

@@ -249,11 +249,23 @@ struct Fp8ProductArgs {
 cudaError_t launch_gemm_fp8(const Fp8ProductArgs& a, cudaStream_t s);
 cudaError_t launch_gemm_fp8_dgrad(const Fp8ProductArgs& a, cudaStream_t s);
 cudaError_t launch_gemm_fp8_wgrad(const Fp8ProductArgs& a, cudaStream_t s);
-// ---- gemm_fp8_few.cu (the same products for few rows per group: tiles of kFewRows rows)
+// ---- gemm_fp8_few.cu (the same products on tiles of kFewRows rows x 128 columns)
 constexpr int kFewRows = 64;
 cudaError_t launch_gemm_fp8_few(const Fp8ProductArgs& a, cudaStream_t s);
 cudaError_t launch_gemm_fp8_dgrad_few(const Fp8ProductArgs& a, cudaStream_t s);
-inline bool use_few_rows(int M, int G) { return (int64_t)M <= (int64_t)kFewRows * G; }
+// Whether they serve this shape (`cols` output columns): a wave of their tiles, one
+// per SM, takes about half as long as a wave of the 128 x 256 tiles, so where
+// they need less than twice the waves.  Measured, K = 6144 x 4096 columns: 64 rows
+// 9.8 against 23.2 us, 256 rows (one wave) 19.7 against 24.3, 384 rows (two) 35.9
+// against 24.9; 32 groups of 16 rows 127 against 143 us, of 64 rows 183 against
+// 144 (the groups' rows vary, so they are taken half as many again).
+inline bool use_few_rows(const Fp8ProductArgs& a, int cols, int sms) {
+    const int64_t groups = a.G < a.M ? a.G : a.M, avg = (a.M + groups - 1) / groups;
+    const int64_t rows = a.offsets == nullptr ? a.M : avg + avg / 2;
+    const int64_t few = groups * ((rows + kFewRows - 1) / kFewRows) * (cols / 128);
+    const int64_t wide = groups * ((rows + 127) / 128) * ((cols + 255) / 256);
+    return (few + sms - 1) / sms < 2 * ((wide + sms - 1) / sms);
+}
 cudaError_t launch_quant_tokens(const uint16_t* x, const int32_t* offsets, int G, int M, int cols,
                                 uint8_t* q, float* scale, cudaStream_t s);
 

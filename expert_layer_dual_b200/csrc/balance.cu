@@ -14,99 +14,103 @@
 // near 1, and the difference of two FP32 values near 1 would keep few bits; f_e - 1
 // = (E c_e - k n) / (k n) has an exact integer numerator.
 //
-// Both kernels give a warp a row, its E <= 256 values in registers (eight per
-// lane), and read and write each value once: bound by HBM for many tokens and by
-// launch latency for few.  Sums are FP32 within a row and over a warp's rows
-// (a few dozen to a few hundred), FP64 over blocks; no atomic on a float, so the
-// results do not depend on scheduling.
+// Eight lanes hold a row, up to 32 values each in registers, so a warp works on
+// four neighbouring rows: the row sums and maxima take three exchanges for four
+// rows, and four rows' loads (up to 4 KB) are in flight per warp.  Every logit is
+// read once and every gradient written once.  With a warp per row (eight values
+// per lane, the accurate expf, the top-k part by comparing every column with
+// every id) both kernels were bound by their instructions, 210 and 496 a row: 41
+// and 82 us for 131072 rows of 256 experts, whose bytes take 20 and 41 us.
+//
+// Sums are FP32 within a row and over a lane's rows, FP64 over the blocks; no
+// atomic on a float, so the results do not depend on scheduling.
 #include "common.cuh"
 #include "launch.h"
 
 namespace moe {
 namespace {
 
-constexpr int kPer = 8;        // values of a row per lane (E <= 256)
-constexpr int kWarps = 8;      // warps per block of the many-block kernels
-constexpr int kOneWarps = 32;  // warps of the one-block kernel
-constexpr int kColBlock = 8;   // experts per block of k_balance_finish
+constexpr int kLanes = 16;               // lanes of a row
+constexpr int kRows = 32 / kLanes;       // rows of a warp
+constexpr int kGroup = 4 * kLanes;       // columns of a row read at once
+constexpr int kWarps = 8;                // warps per block
+constexpr int kOneWarps = 32;            // warps of the one-block kernel
+constexpr int kColBlock = 4;             // experts per block of k_balance_finish
 
-// The column of value i of this lane: VEC: two runs of four consecutive
-// columns per lane (16-byte accesses, E % 4 == 0); else every 32nd column.
-template <bool VEC>
-__device__ __forceinline__ int col_of(int i, int lane) {
-    return VEC ? (i >> 2) * 128 + lane * 4 + (i & 3) : i * 32 + lane;
-}
+// NV: groups of 32 columns (E <= 32 NV); value 4i + c of lane l is column 32i + 4l + c.
+// VEC: E % 4 == 0, so the rows start on 16 bytes.
+__device__ __forceinline__ int col_of(int v, int l) { return (v >> 2) * kGroup + l * 4 + (v & 3); }
 
-template <bool VEC>
-__device__ __forceinline__ void load_row(const float* row, int E, int lane, float* v) {
-    if (VEC) {
+template <int NV, bool VEC>
+__device__ __forceinline__ void load_row(const float* row, int E, int l, float* v) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int c = q * 128 + lane * 4;
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * kGroup + l * 4;
+        if (VEC) {
             float4 f = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
             if (c < E) f = *reinterpret_cast<const float4*>(row + c);
-            v[4 * q] = f.x;
-            v[4 * q + 1] = f.y;
-            v[4 * q + 2] = f.z;
-            v[4 * q + 3] = f.w;
-        }
-    } else {
+            v[4 * i] = f.x;
+            v[4 * i + 1] = f.y;
+            v[4 * i + 2] = f.z;
+            v[4 * i + 3] = f.w;
+        } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int c = i * 32 + lane;
-            v[i] = c < E ? row[c] : -INFINITY;
+            for (int j = 0; j < 4; ++j) v[4 * i + j] = c + j < E ? row[c + j] : -INFINITY;
         }
     }
 }
 
-template <bool VEC>
-__device__ __forceinline__ void store_row(float* __restrict__ row, int E, int lane, const float* v) {
-    if (VEC) {
+template <int NV, bool VEC>
+__device__ __forceinline__ void store_row(float* row, int E, int l, const float* v) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int c = q * 128 + lane * 4;
+    for (int i = 0; i < NV; ++i) {
+        const int c = i * kGroup + l * 4;
+        if (VEC) {
             if (c < E)
                 *reinterpret_cast<float4*>(row + c) =
-                    make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        }
-    } else {
+                    make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int c = i * 32 + lane;
-            if (c < E) row[c] = v[i];
+            for (int j = 0; j < 4; ++j)
+                if (c + j < E) row[c + j] = v[4 * i + j];
         }
     }
 }
 
-__device__ __forceinline__ float warp_max(float v) {
+// Over the eight lanes of a row.
+__device__ __forceinline__ float row_max(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    for (int o = kLanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
     return v;
 }
-__device__ __forceinline__ float warp_sum(float v) {
+__device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
 
-// v <- softmax of the row held across the warp.  A row with no finite logit
-// (every entry -inf) becomes zeros: it selects nothing.
-__device__ __forceinline__ void softmax_row(float* v) {
+// v <- exp(v - max) of the row; returns 1 / sum.  The exponential is the hardware's
+// exp2 of the difference times log2(e): the argument rounds by |l - max| 2^-23, the
+// exponential by 2^-22, as much as the sums around it.  A row without any finite
+// logit (every entry -inf) becomes zeros: it selects nothing.
+template <int N>
+__device__ __forceinline__ float exp_row(float* v) {
     float m = v[0];
 #pragma unroll
-    for (int i = 1; i < kPer; ++i) m = fmaxf(m, v[i]);
-    m = warp_max(m);
+    for (int i = 1; i < N; ++i) m = fmaxf(m, v[i]);
+    m = row_max(m);
     if (m == -INFINITY) m = 0.0f;
+    constexpr float log2e = 1.4426950408889634f;
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        v[i] = expf(v[i] - m);
-        s += v[i];
+    for (int i = 0; i < N; ++i) {
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"((v[i] - m) * log2e));
+        v[i] = e;
+        s += e;
     }
-    s = warp_sum(s);
-    const float inv = s > 0.0f ? 1.0f / s : (s == 0.0f ? 0.0f : s);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] *= inv;
+    s = row_sum(s);
+    return s > 0.0f ? 1.0f / s : (s == 0.0f ? 0.0f : s);  // NaN stays NaN
 }
 
 __device__ __forceinline__ double balance_fraction(int count, int E, double kn) {
@@ -114,142 +118,162 @@ __device__ __forceinline__ double balance_fraction(int count, int E, double kn) 
 }
 
 // ---------------------------------------------------------------------------
-// Loss, first pass: each warp takes every (warps)th token, keeps the sums of
-// its tokens' probabilities in registers (a lane always holds the same
-// columns) and counts the assignments in shared memory (integers); the block's
-// sums go to its row of the partials.  ONE: a single block, which finishes the
-// result itself (few tokens: one launch).
+// Loss, first pass: a warp takes four tokens at a time and keeps the sums of its
+// tokens' probabilities in registers (a lane always holds the same columns);
+// the assignments are counted in shared memory (integers).  The block's sums go
+// to its row of the partials.  ONE: a single block, which finishes the result
+// itself (few tokens: one launch).
 // ---------------------------------------------------------------------------
-template <int WARPS>
-struct RowsSmem {
-    float psum[WARPS][256];
-    int cnt[256];
-    int tokens, bad;
-    double term[8];
-};
-
-template <bool VEC, bool ONE, int WARPS>
+template <int NV, bool VEC, bool ONE, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32)
     k_balance_rows(const float* __restrict__ logits, const int32_t* __restrict__ ids,
                    const uint8_t* __restrict__ mask, int T, int E, int k, BalancePartials part,
                    BalanceOut out) {
-    __shared__ RowsSmem<WARPS> sm;
+    constexpr int N = 4 * NV;
+    __shared__ float s_psum[WARPS][kGroup * NV];
+    __shared__ int s_cnt[256], s_tokens, s_bad;
+    __shared__ double s_term[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int e = tid; e < 256; e += WARPS * 32) sm.cnt[e] = 0;
-    if (tid == 0) sm.tokens = sm.bad = 0;
+    const int l = lane % kLanes, r = lane / kLanes;
+    for (int e = tid; e < 256; e += WARPS * 32) s_cnt[e] = 0;
+    if (tid == 0) s_tokens = s_bad = 0;
     __syncthreads();
     pdl_wait();  // the logits and ids come from the previous kernels
     pdl_trigger();
 
-    float acc[kPer];
+    float acc[N];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
     int tokens = 0, bad = 0;
-    const int step = gridDim.x * WARPS;
-    for (int64_t t0 = blockIdx.x * WARPS + warp; t0 < T; t0 += 2 * (int64_t)step) {
-        // two tokens at a time: two rows in flight per warp
-        float v[2][kPer];
-        bool on[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int64_t t = t0 + (int64_t)u * step;
-            on[u] = t < T && (mask == nullptr || mask[t] != 0);
-            if (on[u]) load_row<VEC>(logits + t * E, E, lane, v[u]);
-            if (on[u] && lane < k) {
-                const int id = ids[t * k + lane];
-                if (id >= 0 && id < E) atomicAdd(&sm.cnt[id], 1);
+    const int64_t step = (int64_t)gridDim.x * WARPS * kRows;
+    for (int64_t t0 = ((int64_t)blockIdx.x * WARPS + warp) * kRows; t0 < T; t0 += step) {
+        const int64_t t = t0 + r;
+        const bool on = t < T && (mask == nullptr || mask[t] != 0);
+        float v[N];
+        if (on) {
+            load_row<NV, VEC>(logits + t * E, E, l, v);
+            if (l < k) {
+                const int id = ids[t * k + l];
+                if (id >= 0 && id < E) atomicAdd(&s_cnt[id], 1);
                 else bad = 1;
             }
+            tokens += l == 0;
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = -INFINITY;
         }
+        const float inv = exp_row<N>(v);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (!on[u]) continue;  // the same for the whole warp
-            softmax_row(v[u]);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) acc[i] += v[u][i];
-            ++tokens;
-        }
+        for (int i = 0; i < N; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
     }
+    // the warp's four rows, then the block's warps
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int c = col_of<VEC>(i, lane);
-        if (c < 256) sm.psum[warp][c] = acc[i];
+    for (int i = 0; i < N; ++i) {
+        for (int o = kLanes; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
     }
-    if (bad) sm.bad = 1;
-    if (lane == 0 && tokens) atomicAdd(&sm.tokens, tokens);
+    if (r == 0)
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            *reinterpret_cast<float4*>(&s_psum[warp][i * kGroup + l * 4]) =
+                make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+    tokens = __reduce_add_sync(0xffffffffu, tokens);
+    if (bad) s_bad = 1;
+    if (lane == 0 && tokens) atomicAdd(&s_tokens, tokens);
     __syncthreads();
 
     if (!ONE) {
         for (int e = tid; e < E; e += WARPS * 32) {
             float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) s += sm.psum[w][e];
+            for (int w = 0; w < WARPS; ++w) s += s_psum[w][e];
             part.psum[(int64_t)blockIdx.x * E + e] = s;
-            part.cnt[(int64_t)blockIdx.x * E + e] = sm.cnt[e];
+            part.cnt[(int64_t)blockIdx.x * E + e] = s_cnt[e];
         }
         if (tid == 0) {
-            part.info[2 * blockIdx.x] = sm.tokens;
-            part.info[2 * blockIdx.x + 1] = sm.bad;
+            part.info[2 * blockIdx.x] = s_tokens;
+            part.info[2 * blockIdx.x + 1] = s_bad;
             if (blockIdx.x == 0) *part.arrived = 0;
         }
         return;
     }
+    const int n = s_tokens;
     double term = 0.0;
     if (tid < 256) {
-        const int n = sm.tokens;
         if (tid < E) {
             float s = 0.0f;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) s += sm.psum[w][tid];
+            for (int w = 0; w < WARPS; ++w) s += s_psum[w][tid];
             const double mean = n > 0 ? (double)s / n : 0.0;
             out.prob_mean[tid] = (float)mean;
-            out.counts[tid] = sm.cnt[tid];
-            term = balance_fraction(sm.cnt[tid], E, (double)k * n) * mean;
+            out.counts[tid] = s_cnt[tid];
+            term = balance_fraction(s_cnt[tid], E, (double)k * n) * mean;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
-        if (lane == 0) sm.term[warp] = term;
+        if (lane == 0) s_term[warp] = term;
     }
     __syncthreads();
     if (tid == 0) {
         double s = 0.0;
-        for (int w = 0; w < 8; ++w) s += sm.term[w];
+        for (int w = 0; w < 8; ++w) s += s_term[w];
         *out.loss = (float)(out.coef * s);
-        *out.tokens = sm.tokens;
-        *out.status = sm.bad ? MOE_ERR_DEVICE_BAD_INDEX : MOE_OK;
+        *out.tokens = n;
+        *out.status = s_bad ? MOE_ERR_DEVICE_BAD_INDEX : MOE_OK;
     }
 }
 
 // Loss, second pass: a block sums the partials of kColBlock experts over the
-// first pass's blocks (in FP64, a fixed order) and leaves each expert's share
-// of the loss; the last block to arrive adds the E shares in order.
+// first pass's blocks (in FP64, a fixed order; every load of a thread in flight
+// together) and leaves each expert's share of the loss; the last block to arrive
+// adds the E shares in order.
 __global__ void __launch_bounds__(256)
     k_balance_finish(int E, int k, int nblocks, BalancePartials part, BalanceOut out) {
-    __shared__ double s_sum[32][kColBlock];
-    __shared__ int s_cnt[32][kColBlock];
+    constexpr int SLICES = 256 / kColBlock, PER = (kBalanceMaxBlocks + SLICES - 1) / SLICES;
+    __shared__ double s_sum[SLICES][kColBlock];
+    __shared__ int s_cnt[SLICES][kColBlock];
     __shared__ int s_tokens[8], s_bad[8], s_last;
     __shared__ double s_term[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_trigger();
     const int e = blockIdx.x * kColBlock + tid % kColBlock, slice = tid / kColBlock;
+    float p[PER];
+    int c[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int b = slice + i * SLICES;
+        const bool in = e < E && b < nblocks;
+        p[i] = in ? part.psum[(int64_t)b * E + e] : 0.0f;
+        c[i] = in ? part.cnt[(int64_t)b * E + e] : 0;
+    }
+    int tokens = 0, bad = 0;
+#pragma unroll
+    for (int i = 0; i < (kBalanceMaxBlocks + 255) / 256; ++i) {
+        const int b = tid + 256 * i;
+        if (b < nblocks) {
+            tokens += part.info[2 * b];
+            bad |= part.info[2 * b + 1];
+        }
+    }
     double sum = 0.0;
     int cnt = 0;
-    if (e < E)
-#pragma unroll 4
-        for (int b = slice; b < nblocks; b += 32) {
-            sum += part.psum[(int64_t)b * E + e];
-            cnt += part.cnt[(int64_t)b * E + e];
-        }
-    int tokens = 0, bad = 0;
-    for (int b = tid; b < nblocks; b += 256) {
-        tokens += part.info[2 * b];
-        bad |= part.info[2 * b + 1];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        sum += p[i];
+        cnt += c[i];
+    }
+    // slices of the same expert within the warp (lanes kColBlock apart), then over the warps
+#pragma unroll
+    for (int o = kColBlock; o < 32; o <<= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
     }
     tokens = __reduce_add_sync(0xffffffffu, tokens);
     bad = __reduce_or_sync(0xffffffffu, bad);
-    s_sum[slice][tid % kColBlock] = sum;
-    s_cnt[slice][tid % kColBlock] = cnt;
+    if (lane < kColBlock) {
+        s_sum[warp][lane] = sum;
+        s_cnt[warp][lane] = cnt;
+    }
     if (lane == 0) {
         s_tokens[warp] = tokens;
         s_bad[warp] = bad;
@@ -262,17 +286,17 @@ __global__ void __launch_bounds__(256)
     }
     if (tid < kColBlock && e < E) {
         double s = 0.0;
-        int c = 0;
-        for (int i = 0; i < 32; ++i) {
-            s += s_sum[i][tid];
-            c += s_cnt[i][tid];
+        int m = 0;
+        for (int w = 0; w < 8; ++w) {
+            s += s_sum[w][tid];
+            m += s_cnt[w][tid];
         }
         const double mean = n > 0 ? s / n : 0.0;
         out.prob_mean[e] = (float)mean;
-        out.counts[e] = c;
-        part.term[e] = balance_fraction(c, E, (double)k * n) * mean;
+        out.counts[e] = m;
+        part.term[e] = balance_fraction(m, E, (double)k * n) * mean;
+        __threadfence();
     }
-    __threadfence();
     __syncthreads();
     if (tid == 0) s_last = atomicAdd(part.arrived, 1) == (int)gridDim.x - 1;
     __syncthreads();
@@ -293,115 +317,171 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------------------
-// Gradient of the logits: a warp per row, the softmax recomputed from the
-// logits (cheaper than a saved row: nothing more is read).  Masked tokens get
-// zeros and their logits are not read.
+// Gradient of the logits: four rows per warp as above, the softmax recomputed
+// from the logits (nothing more is read).  The k values of the top-k part go to
+// their columns through a row of shared memory that is zero in between; ids that
+// repeat within a row are added up first, so their order does not matter.
+// Masked tokens get zeros and their logits are not read.
 // ---------------------------------------------------------------------------
-template <bool VEC>
+template <int NV, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32)
-    k_route_backward(RouteBackwardArgs a) {
+    k_route_backward(const __grid_constant__ RouteBackwardArgs a) {
+    constexpr int N = 4 * NV;
+    __shared__ float s_row[kWarps][kRows][kGroup * NV];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int l = lane % kLanes, r = lane / kLanes;
+    float* const srow = s_row[warp][r];
+    for (int c = l; c < kGroup * NV; c += kLanes) srow[c] = 0.0f;
+    __syncwarp();
     pdl_wait();
     pdl_trigger();
     const int E = a.E, k = a.k;
     const bool balance = a.dloss != nullptr, need_p = balance || !a.renorm;
-    float f1[kPer], cb = 0.0f;  // f_e - 1 of this lane's columns; dloss coef / n
+    float f1[N], cb = 0.0f;  // f_e - 1 of this lane's columns; dloss coef / n
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) f1[i] = 0.0f;
+    for (int i = 0; i < N; ++i) f1[i] = 0.0f;
     if (balance) {
         const int n = *a.tokens;
         const double kn = (double)k * n;
         cb = n > 0 ? (float)((double)*a.dloss * a.coef / n) : 0.0f;
+        const double inv = n > 0 ? 1.0 / kn : 0.0;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int c = col_of<VEC>(i, lane);
-            if (c < E && n > 0) f1[i] = (float)(((double)a.counts[c] * E - kn) / kn);
+        for (int i = 0; i < N; ++i) {
+            const int c = col_of(i, l);
+            if (c < E) f1[i] = (float)(((double)a.counts[c] * E - kn) * inv);
         }
     }
-    const int step = gridDim.x * kWarps;
-    for (int64_t t = blockIdx.x * kWarps + warp; t < a.T; t += step) {
-        float g[kPer];
-        if (a.mask != nullptr && a.mask[t] == 0) {
+    const int64_t step = (int64_t)gridDim.x * kWarps * kRows;
+    for (int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kRows; t0 < a.T; t0 += step) {
+        const int64_t t = t0 + r;
+        const bool in = t < a.T, on = in && (a.mask == nullptr || a.mask[t] != 0);
+        float p[N];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) g[i] = 0.0f;
-            store_row<VEC>(a.dlogits + t * E, E, lane, g);
-            continue;
-        }
-        float p[kPer];
-        if (need_p) load_row<VEC>(a.logits + t * E, E, lane, p);
+        for (int i = 0; i < N; ++i) p[i] = -INFINITY;
+        if (need_p && on) load_row<NV, VEC>(a.logits + t * E, E, l, p);
         int id = -1;
         float w = 0.0f, d = 0.0f;
-        if (a.dw != nullptr && lane < k) {
-            id = a.ids[t * k + lane];
-            w = a.w[t * k + lane];
-            d = a.dw[t * k + lane];
+        if (a.dw != nullptr && on && l < k) {
+            id = a.ids[t * k + l];
+            w = a.w[t * k + l];
+            d = a.dw[t * k + l];
         }
-        if (need_p) softmax_row(p);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) g[i] = 0.0f;
+        float inv = 0.0f, dot = 0.0f;
+        if (need_p) inv = exp_row<N>(p);
         if (a.dw != nullptr) {
-            const float dot = warp_sum(w * d);
+            dot = row_sum(w * d);
             const float mine = a.renorm ? w * (d - dot) : d;
+            float sum = 0.0f;  // of the row's lanes with this id; the first of them writes
+            bool first = true;
             for (int j = 0; j < k; ++j) {
-                const int idj = __shfl_sync(0xffffffffu, id, j);
-                const float gj = __shfl_sync(0xffffffffu, mine, j);
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (idj == col_of<VEC>(i, lane)) g[i] += gj;
+                const int idj = __shfl_sync(0xffffffffu, id, j, kLanes);
+                const float vj = __shfl_sync(0xffffffffu, mine, j, kLanes);
+                if (idj == id) {
+                    sum += vj;
+                    first = first && j >= l;
+                }
             }
-            if (!a.renorm) {
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) g[i] = p[i] * (g[i] - dot);
-            }
+            if (first && id >= 0 && id < E) srow[id] = sum;
+            __syncwarp();
         }
+        float s = 0.0f;
         if (balance) {
-            float s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) s = fmaf(f1[i], p[i], s);
-            s = warp_sum(s);
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) g[i] = fmaf(cb * p[i], f1[i] - s, g[i]);
+            for (int i = 0; i < N; ++i) s = fmaf(f1[i], p[i], s);
+            s = row_sum(s) * inv;
         }
-        store_row<VEC>(a.dlogits + t * E, E, lane, g);
+        const float ci = cb * inv;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float g[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (a.dw != nullptr) {
+                const float4 q = *reinterpret_cast<const float4*>(srow + i * kGroup + l * 4);
+                g[0] = q.x;
+                g[1] = q.y;
+                g[2] = q.z;
+                g[3] = q.w;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float e = p[4 * i + j];
+                if (!a.renorm) g[j] = e * inv * (g[j] - dot);
+                if (balance) g[j] = fmaf(ci * e, f1[4 * i + j] - s, g[j]);
+                p[4 * i + j] = on ? g[j] : 0.0f;
+            }
+        }
+        if (in) store_row<NV, VEC>(a.dlogits + t * E, E, l, p);
+        if (a.dw != nullptr) {
+            __syncwarp();
+            if (id >= 0 && id < E) srow[id] = 0.0f;
+            __syncwarp();
+        }
     }
 }
 
-inline bool vec_ok(int E) { return E % 4 == 0; }
+// The instance for E experts: groups of 32 columns rounded up to 1, 2, 4 or 8.
+template <typename F>
+cudaError_t by_width(int E, F f) {
+    const bool vec = E % 4 == 0;
+    if (E <= kGroup) return vec ? f.template operator()<1, true>() : f.template operator()<1, false>();
+    if (E <= 2 * kGroup) return vec ? f.template operator()<2, true>() : f.template operator()<2, false>();
+    return vec ? f.template operator()<4, true>() : f.template operator()<4, false>();
+}
+
+struct LaunchRows {
+    const float* logits;
+    const int32_t* ids;
+    const uint8_t* mask;
+    int T, E, k, blocks;
+    BalancePartials part;
+    BalanceOut out;
+    cudaStream_t s;
+    template <int NV, bool VEC>
+    cudaError_t operator()() const {
+        if (blocks == 1)
+            return launch_pdl(k_balance_rows<NV, VEC, true, kOneWarps>, dim3(1), dim3(kOneWarps * 32), 0, s,
+                              logits, ids, mask, T, E, k, part, out);
+        return launch_pdl(k_balance_rows<NV, VEC, false, kWarps>, dim3(blocks), dim3(kWarps * 32), 0, s,
+                          logits, ids, mask, T, E, k, part, out);
+    }
+};
+
+struct LaunchBackward {
+    RouteBackwardArgs a;
+    cudaStream_t s;
+    template <int NV, bool VEC>
+    cudaError_t operator()() const {
+        const int64_t want = ((int64_t)a.T + kWarps * kRows - 1) / (kWarps * kRows);
+        const int64_t most = (int64_t)current_device_info().num_sms * 6;
+        return launch_pdl(k_route_backward<NV, VEC>, dim3((unsigned)(want < most ? want : most)),
+                          dim3(kWarps * 32), 0, s, a);
+    }
+};
 
 }  // namespace
 
 int balance_blocks(int T) {
     if (T <= kBalanceOneBlock) return 1;
-    const int want = (T + 2 * kWarps - 1) / (2 * kWarps);
-    return want < kBalanceMaxBlocks ? want : kBalanceMaxBlocks;
+    // a block per 64 tokens (the second pass reads a row of partials per block: with
+    // one per 16 16384 tokens took 11.2 us, so 8.7), but one per SM as soon as
+    // each has a turn's tokens
+    const int64_t few = ((int64_t)T + kWarps * kRows - 1) / (kWarps * kRows), many = ((int64_t)T + 63) / 64;
+    const int64_t want = few < 148 ? few : many < 148 ? 148 : many;
+    return want < kBalanceMaxBlocks ? (int)want : kBalanceMaxBlocks;
 }
 
 cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, const uint8_t* mask, int T,
                                 int E, int k, const BalancePartials& part, const BalanceOut& out,
                                 cudaStream_t s) {
     const int nb = balance_blocks(T);
-    cudaError_t e;
-    if (nb == 1) {
-        e = launch_pdl(vec_ok(E) ? k_balance_rows<true, true, kOneWarps>
-                                 : k_balance_rows<false, true, kOneWarps>,
-                       dim3(1), dim3(kOneWarps * 32), 0, s, logits, ids, mask, T, E, k, part, out);
-        return e != cudaSuccess ? e : cudaGetLastError();
-    }
-    e = launch_pdl(vec_ok(E) ? k_balance_rows<true, false, kWarps>
-                             : k_balance_rows<false, false, kWarps>,
-                   dim3(nb), dim3(kWarps * 32), 0, s, logits, ids, mask, T, E, k, part, out);
-    if (e != cudaSuccess) return e;
+    cudaError_t e = by_width(E, LaunchRows{logits, ids, mask, T, E, k, nb, part, out, s});
+    if (e != cudaSuccess || nb == 1) return e != cudaSuccess ? e : cudaGetLastError();
     e = launch_pdl(k_balance_finish, dim3((E + kColBlock - 1) / kColBlock), dim3(256), 0, s, E, k, nb,
                    part, out);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_route_backward(const RouteBackwardArgs& a, cudaStream_t s) {
-    const int64_t want = ((int64_t)a.T + kWarps - 1) / kWarps;
-    const int64_t most = (int64_t)current_device_info().num_sms * 8;
-    const cudaError_t e =
-        launch_pdl(vec_ok(a.E) ? k_route_backward<true> : k_route_backward<false>,
-                   dim3((unsigned)(want < most ? want : most)), dim3(kWarps * 32), 0, s, a);
+    const cudaError_t e = by_width(a.E, LaunchBackward{a, s});
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -270,7 +270,7 @@ cudaError_t launch_quant_tokens(const uint16_t* x, const int32_t* offsets, int G
                                 uint8_t* q, float* scale, cudaStream_t s);
 
 // ---- balance.cu (load-balance loss, per-expert counts, gradient of the router logits)
-constexpr int kBalanceOneBlock = 512;   // up to this many tokens one block does it all
+constexpr int kBalanceOneBlock = 128;   // up to this many tokens one block does it all
 constexpr int kBalanceMaxBlocks = 592;  // blocks of the first pass (four per SM)
 struct BalancePartials {                // workspace of the two-pass form
     float* psum;       // [blocks][E]

@@ -1,4 +1,5 @@
-"""Builds the sm_100a shared library libmoe_b200.so in-tree with nvcc.
+"""Builds the sm_100a shared library libmoe_b200.so in-tree with nvcc, and the
+native Python binding _moe_binding.so with g++.
 
     python -m expert_layer_dual_b200.build [--force]
 
@@ -19,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_b200.so")
+BINDING = os.path.join(HERE, "_moe_binding.so")
 SOURCES = ["api.cu", "routing.cu", "router.cu", "gemm_bf16.cu", "gemm_bf16_wide.cu", "gemm_bf16_2sm.cu", "gemm_fp8.cu", "gemm_mx.cu", "gemm_f8t.cu", "gemm_fp8_block.cu", "gemm_fp8_few.cu",
            "ep.cu", "allreduce_norm.cu", "noalloc.cu", "balance.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -71,7 +73,38 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         os.replace(tmp, LIB)
         if verbose:
             print("built", LIB)
+    build_binding(force, verbose)
     return LIB
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The native argument marshalling (csrc/binding.cpp): a CPython module against
+    this interpreter and its torch, linked to the library next to it."""
+    import sysconfig
+    import torch
+    src = os.path.join(CSRC, "binding.cpp")
+    stamp = os.path.join(BUILD, "binding.stamp")
+    made_with = f"{sys.version} torch {torch.__version__}"
+    same = os.path.exists(stamp) and open(stamp).read() == made_with
+    newest = max(_mtime(src), _mtime(os.path.join(INCLUDE, "moe.h")))
+    if force or not same or _mtime(BINDING) < newest:
+        t = os.path.dirname(torch.__file__)
+        tmp = BINDING + f".tmp{os.getpid()}"
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               "-I", os.path.join(t, "include"),
+               "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+               "-I", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", HERE, "-l:libmoe_b200.so",
+               "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, BINDING)
+        with open(stamp, "w") as f:
+            f.write(made_with)
+        if verbose:
+            print("built", BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

@@ -1,4 +1,6 @@
-"""ctypes binding of libmoe_b200.so (the C ABI in include/moe.h).
+"""Binding of libmoe_b200.so (the C ABI in include/moe.h): ctypes, and for the
+training entry points, whose small calls are bound by their marshalling, the
+native module _moe_binding (csrc/binding.cpp).
 
 Argument marshalling only: every function here hands device pointers, sizes
 and the current CUDA stream to the entry point of the same name and raises
@@ -12,6 +14,7 @@ shared library has not been built (``python -m expert_layer_dual_b200.build``).
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
@@ -26,6 +29,19 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is missing: build it with `python -m expert_layer_dual_b200.build`")
 
 _lib = ctypes.CDLL(LIB_PATH)
+
+
+def _load_native():
+    path = os.path.join(_HERE, "_moe_binding.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with `python -m expert_layer_dual_b200.build`")
+    spec = importlib.util.spec_from_file_location("_moe_binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+_native = _load_native()
 
 OK, INVALID_ARG, UNSUPPORTED, CUDA_ERROR, WORKSPACE_TOO_SMALL, DEVICE_TIMEOUT, DEVICE_BAD_INDEX = range(7)
 WDTYPE_BF16, WDTYPE_FP8_BLOCK128, WDTYPE_MXFP8, WDTYPE_FP8_TENSOR = 0, 1, 2, 3
@@ -156,17 +172,18 @@ def _p(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr()) if t.numel() else None
 
 
-# The current stream's handle without building a torch.cuda.Stream (3.5 us a call).
-_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current device and its current stream's handle without the Python layers
+# around them (a torch.cuda.Stream object alone takes 3.5 us to build).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _stream(stream) -> int:
-    """cudaStream_t of `stream` (None: the current one) as an integer."""
-    if stream is not None:
-        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if _current_raw_stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return _current_raw_stream(torch.cuda.current_device())
+def _stream(stream, dev=None) -> int:
+    """cudaStream_t of `stream` (None: the current one, of device `dev`) as an integer."""
+    if stream is None:
+        return _current_raw_stream(torch.cuda.current_device() if dev is None else dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def shape_of(cfg: MoEConfig, T: Optional[int] = None) -> moe_shape:
@@ -326,9 +343,8 @@ def quantize_weights_fp8(W, q, scale, stream=None):
 
 
 def quantize_act_fp8(x, q, scale, stream=None):
-    rows, cols = x.shape
-    _check(_lib.moe_quantize_act_fp8(_p(x), rows, cols, _p(q), _p(scale), _stream(stream)),
-           "moe_quantize_act_fp8")
+    dev = _launch_device(x)
+    _check(_native.quantize_act_fp8(dev, _stream(stream, dev), x, q, scale), "moe_quantize_act_fp8")
 
 
 def quantize_weights_mxfp8(W, q, scale, stream=None):
@@ -428,39 +444,15 @@ def forward(shape, weights, x, y, ws, stream=None):
 
 
 # ------------------------------------------------------------------ training entry points
-_OUT_TYPES = {torch.bfloat16: OUT_BF16, torch.uint16: OUT_BF16, torch.float16: OUT_F16,
-              torch.float32: OUT_F32}
-
-
-def _arg(name, t, shape, dtypes, dev):
-    """Device address of a tensor of the call; refuses one whose shape, type,
-    layout or device is not the call's."""
-    if t.shape != shape or t.dtype not in dtypes or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype} on {t.device}, contiguous: "
-                         f"{t.is_contiguous()}; expected {tuple(shape)} {' or '.join(map(str, dtypes))} "
-                         f"on cuda:{dev}, contiguous")
-    return t.data_ptr()
-
-
-def _launch_device(t):
+# The native binding checks every tensor (shape, type, contiguity, the current
+# device) and raises ValueError on one that is not the call's.
+def _launch_device(t) -> int:
     """The index of the current device, on which the library launches: the
     call's tensors have to be there."""
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _current_device():
         raise ValueError(f"the tensors are on {t.device}, not on the current CUDA device")
     return dev
-
-
-def _ws(ws, dev):
-    if ws.get_device() != dev or not ws.is_contiguous():
-        raise ValueError("workspace: not a contiguous tensor on the current CUDA device")
-    return ws.data_ptr(), ws.numel() * ws.element_size()
-
-
-_F32, _I32 = (torch.float32,), (torch.int32,)
-_CODES = (torch.uint8, torch.float8_e4m3fn)
-_BF16 = (torch.bfloat16, torch.uint16)
-_MASK = (torch.uint8, torch.bool)
 
 
 def balance_workspace_bytes(T: int, E: int) -> int:
@@ -471,14 +463,8 @@ def balance_loss(logits, ids, mask, coef, loss, counts, prob_mean, tokens, ws, s
     """moe_balance_loss: loss [1], counts [E], prob_mean [E] and tokens [1] of
     logits [T, E] and the selected ids [T, k]; mask [T] (uint8 or bool) or None."""
     dev = _launch_device(logits)
-    T, E = logits.shape
-    k = ids.shape[1]
-    _check(_lib.moe_balance_loss(
-        _arg("logits", logits, (T, E), _F32, dev), _arg("ids", ids, (T, k), _I32, dev),
-        None if mask is None else _arg("mask", mask, (T,), _MASK, dev), T, E, k, coef,
-        _arg("loss", loss, (1,), _F32, dev), _arg("counts", counts, (E,), _I32, dev),
-        _arg("prob_mean", prob_mean, (E,), _F32, dev), _arg("tokens", tokens, (1,), _I32, dev),
-        *_ws(ws, dev), _stream(stream)), "moe_balance_loss")
+    _check(_native.balance_loss(dev, _stream(stream, dev), logits, ids, mask, coef, loss, counts, prob_mean,
+                                tokens, ws), "moe_balance_loss")
 
 
 def route_backward(logits, ids, w, dw, mask, renormalize, dloss, coef, counts, tokens, dlogits,
@@ -488,56 +474,24 @@ def route_backward(logits, ids, w, dw, mask, renormalize, dloss, coef, counts, t
     (None: without it); w may be None without dw, counts and tokens without
     dloss."""
     dev = _launch_device(logits)
-    T, E = logits.shape
-    k = ids.shape[1]
-    a = (_arg("logits", logits, (T, E), _F32, dev), _arg("ids", ids, (T, k), _I32, dev))
-    parts = (None, None) if dw is None else (_arg("w", w, (T, k), _F32, dev),
-                                             _arg("dw", dw, (T, k), _F32, dev))
-    aux = (None, None, None) if dloss is None else (_arg("dloss", dloss, (1,), _F32, dev),
-                                                    _arg("counts", counts, (E,), _I32, dev),
-                                                    _arg("tokens", tokens, (1,), _I32, dev))
-    _check(_lib.moe_route_backward(
-        *a, *parts, None if mask is None else _arg("mask", mask, (T,), _MASK, dev), T, E, k,
-        1 if renormalize else 0, aux[0], coef, aux[1], aux[2],
-        _arg("dlogits", dlogits, (T, E), _F32, dev), _stream(stream)), "moe_route_backward")
-
-
-def _weight_shape(w_q, offsets):
-    """(G, N, K) of weight codes [N, K] or [G, N, K]."""
-    shape = w_q.shape
-    G = shape[0] if len(shape) == 3 else 1
-    if offsets is None and G != 1:
-        raise ValueError("several weight matrices need offsets")
-    return G, shape[-2], shape[-1]
-
-
-def _product(entry, name, a_q, a_s, w_q, w_s, offsets, out, a_cols, out_cols, G, N, K, ws, stream):
-    dev = _launch_device(a_q)
-    M = a_q.shape[0]
-    _check(entry(
-        _arg("codes", a_q, (M, a_cols), _CODES, dev), _arg("scales", a_s, (M, a_cols // 128), _F32, dev),
-        _arg("weight codes", w_q, w_q.shape, _CODES, dev),
-        _arg("weight scales", w_s, w_q.shape[:-2] + (N // 128, K // 128), _F32, dev),
-        None if offsets is None else _arg("offsets", offsets, (G + 1,), _I32, dev), G, M, N, K,
-        _arg("output", out, (M, out_cols), _OUT_TYPES, dev), _OUT_TYPES[out.dtype], *_ws(ws, dev),
-        _stream(stream)), name)
+    _check(_native.route_backward(dev, _stream(stream, dev), logits, ids, w, dw, mask, renormalize, dloss, coef,
+                                  counts, tokens, dlogits), "moe_route_backward")
 
 
 def gemm_fp8(x_q, x_s, w_q, w_s, offsets, y, ws, stream=None):
     """moe_gemm_fp8: y [M, N] (bf16, f16 or f32) = x W^T from e4m3 codes x_q
     [M, K], w_q [N, K] or [G, N, K] and their 1x128 / 128x128 scales; offsets
     [G+1] (int32) or None for one matrix."""
-    G, N, K = _weight_shape(w_q, offsets)
-    _product(_lib.moe_gemm_fp8, "moe_gemm_fp8", x_q, x_s, w_q, w_s, offsets, y, K, N, G, N, K, ws,
-             stream)
+    dev = _launch_device(x_q)
+    _check(_native.gemm_fp8(dev, _stream(stream, dev), x_q, x_s, w_q, w_s, offsets, y, ws), "moe_gemm_fp8")
 
 
 def gemm_fp8_dgrad(dy_q, dy_s, w_q, w_s, offsets, dx, ws, stream=None):
     """moe_gemm_fp8_dgrad: dx [M, K] = dy W from dy's codes [M, N] and the
     forward's weight codes and scales."""
-    G, N, K = _weight_shape(w_q, offsets)
-    _product(_lib.moe_gemm_fp8_dgrad, "moe_gemm_fp8_dgrad", dy_q, dy_s, w_q, w_s, offsets, dx, N, K, G,
-             N, K, ws, stream)
+    dev = _launch_device(dy_q)
+    _check(_native.gemm_fp8_dgrad(dev, _stream(stream, dev), dy_q, dy_s, w_q, w_s, offsets, dx, ws),
+           "moe_gemm_fp8_dgrad")
 
 
 def fp8_token_rows(M: int, G: int = 1) -> int:
@@ -548,28 +502,16 @@ def quantize_fp8_tokens(x, offsets, q_t, scale_t, stream=None):
     """moe_quantize_fp8_tokens: x [M, cols] (bf16) -> q_t [cols, R] e4m3 codes,
     scale_t [R/128, cols], R = fp8_token_rows(M, G)."""
     dev = _launch_device(x)
-    M, cols = x.shape
-    G = 1 if offsets is None else offsets.shape[0] - 1
-    R = _lib.moe_fp8_token_rows(M, G)
-    _check(_lib.moe_quantize_fp8_tokens(
-        _arg("x", x, (M, cols), _BF16, dev),
-        None if offsets is None else _arg("offsets", offsets, (G + 1,), _I32, dev), G, M, cols,
-        _arg("codes", q_t, (cols, R), _CODES, dev), _arg("scales", scale_t, (R // 128, cols), _F32, dev),
-        _stream(stream)), "moe_quantize_fp8_tokens")
+    _check(_native.quantize_fp8_tokens(dev, _stream(stream, dev), x, offsets, q_t, scale_t),
+           "moe_quantize_fp8_tokens")
 
 
 def gemm_fp8_wgrad(dy_t, dy_ts, x_t, x_ts, offsets, M, dw, accumulate, ws, stream=None):
     """moe_gemm_fp8_wgrad: dw [N, K] or [G, N, K] (f32) = (or +=, accumulate)
     dy^T x over each group's rows, from quantize_fp8_tokens' outputs."""
     dev = _launch_device(dw)
-    G, N, K = _weight_shape(dw, offsets)
-    R = _lib.moe_fp8_token_rows(M, G)
-    _check(_lib.moe_gemm_fp8_wgrad(
-        _arg("dy codes", dy_t, (N, R), _CODES, dev), _arg("dy scales", dy_ts, (R // 128, N), _F32, dev),
-        _arg("x codes", x_t, (K, R), _CODES, dev), _arg("x scales", x_ts, (R // 128, K), _F32, dev),
-        None if offsets is None else _arg("offsets", offsets, (G + 1,), _I32, dev), G, M, N, K,
-        _arg("dw", dw, dw.shape, _F32, dev), 1 if accumulate else 0, *_ws(ws, dev), _stream(stream)),
-           "moe_gemm_fp8_wgrad")
+    _check(_native.gemm_fp8_wgrad(dev, _stream(stream, dev), dy_t, dy_ts, x_t, x_ts, offsets, M, dw, accumulate,
+                                  ws), "moe_gemm_fp8_wgrad")
 
 
 PROFILE_EVENTS = 8

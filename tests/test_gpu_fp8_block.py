@@ -388,3 +388,36 @@ def test_scale_of_every_bf16_maximum():
     M.quantize_act_fp8(x.to(DEV), q, s)
     wq, ws = ref.quantise_rows(x)
     assert torch.equal(s.cpu(), ws) and torch.equal(q.cpu(), wq)
+
+
+def test_binding_refuses_what_is_not_the_calls():
+    """Shapes, types, layouts and devices that do not fit raise ValueError before a
+    launch; limits of the library come back as its status."""
+    z = lambda *s, d=torch.uint8: torch.zeros(s, dtype=d, device=DEV)  # noqa: E731
+    f32 = torch.float32
+    good = dict(x_q=z(4, 256), x_s=z(4, 2, d=f32), w_q=z(128, 256), w_s=z(1, 2, d=f32), offsets=None,
+                y=z(4, 128, d=f32), ws=z(256))
+    M.gemm_fp8(*good.values())
+    for change in ({"x_q": z(256, 4).T}, {"x_q": z(4, 128)}, {"x_q": z(4, 256, d=f32)}, {"x_s": z(4, 3, d=f32)},
+                   {"x_s": z(2, 4, d=f32)}, {"x_s": z(4, 2, d=torch.float64)}, {"w_q": z(128, 256).cpu()},
+                   {"w_s": z(2, 1, d=f32)}, {"y": z(4, 256, d=f32)}, {"y": z(4, 128, d=torch.int32)},
+                   {"y": z(4, 256, d=f32)[:, ::2]}, {"offsets": z(2, d=torch.int64)},
+                   {"offsets": z(3, d=torch.int32)}, {"w_q": z(2, 128, 256), "w_s": z(2, 1, 2, d=f32)},
+                   {"ws": z(256).cpu()}, {"x_q": None}):
+        with pytest.raises((ValueError, AttributeError)):
+            M.gemm_fp8(*{**good, **change}.values())
+    for change, code in (({"ws": z(128)}, M.WORKSPACE_TOO_SMALL),
+                         ({"w_q": z(100, 256), "w_s": z(0, 2, d=f32), "y": z(4, 100, d=f32)}, M.UNSUPPORTED),
+                         ({"x_q": z(4 * 256 + 8)[8:].view(4, 256)}, M.INVALID_ARG)):
+        with pytest.raises(M.MoEError) as e:
+            M.gemm_fp8(*{**good, **change}.values())
+        assert e.value.code == code
+    dw, t, ts = z(128, 256, d=f32), z(128, 128), z(1, 128, d=f32)
+    xt, xts = z(256, 128), z(1, 256, d=f32)
+    M.gemm_fp8_wgrad(t, ts, xt, xts, None, 5, dw, False, z(256))
+    for bad in ((t, ts, xt, xts, None, 129, dw, False, z(256)), (xt, ts, xt, xts, None, 5, dw, False, z(256)),
+                (t, ts, xt, xts, None, 5, dw.half(), False, z(256))):
+        with pytest.raises(ValueError):
+            M.gemm_fp8_wgrad(*bad)
+    with pytest.raises(M.MoEError):
+        M.gemm_fp8_wgrad(z(128, 0), z(0, 128, d=f32), z(256, 0), z(0, 256, d=f32), None, -1, dw, False, z(256))

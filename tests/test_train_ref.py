@@ -199,6 +199,34 @@ def test_binding_refuses_tensors_off_the_current_device(M):
     with pytest.raises(ValueError, match="current CUDA device"):
         M.gemm_fp8(t, s, torch.zeros((128, 128), dtype=torch.uint8), torch.zeros((1, 1)), None,
                    torch.zeros((4, 128)), torch.zeros(256, dtype=torch.uint8))
-    with pytest.raises(ValueError, match="offsets"):
-        M.gemm_fp8(t, s, torch.zeros((2, 128, 128), dtype=torch.uint8), torch.zeros((2, 1, 1)), None,
-                   torch.zeros((4, 128)), torch.zeros(256, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="current CUDA device"):
+        M.balance_loss(s, t, None, 0.1, s, t, s, t, t)
+
+
+def test_native_binding_checks_before_it_calls(M):
+    """The native layer itself (device 0, stream 0): nothing is launched for
+    tensors elsewhere, of another rank, or that are no tensors."""
+    n = M._native
+    t, s = torch.zeros((4, 128), dtype=torch.uint8), torch.zeros((4, 1))
+    w, ws = torch.zeros((128, 128), dtype=torch.uint8), torch.zeros((1, 1))
+    for f in (n.gemm_fp8, n.gemm_fp8_dgrad):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            f(0, 0, t, s, w, ws, None, s, t)
+        with pytest.raises(ValueError, match="a matrix"):
+            f(0, 0, t[0], s, w, ws, None, s, t)
+        with pytest.raises(ValueError, match="not a tensor"):
+            f(0, 0, t, s, None, ws, None, s, t)
+        with pytest.raises(ValueError, match="offsets"):
+            f(0, 0, t, s, torch.zeros((2, 128, 128), dtype=torch.uint8), ws, None, s, t)
+        with pytest.raises(TypeError):
+            f(0, 0, t)
+    with pytest.raises(ValueError):
+        n.quantize_act_fp8(0, 0, torch.zeros((4, 128)).to_sparse(), t, s)
+    with pytest.raises(ValueError):
+        n.quantize_fp8_tokens(0, 0, torch.zeros((4, 128), device="meta"), None, t, s)
+    with pytest.raises(ValueError):
+        n.route_backward(0, 0, s, t, None, None, None, True, s, 0.1, t, t, s)
+    with pytest.raises(ValueError):
+        n.gemm_fp8_wgrad(0, 0, t, s, t, s, None, 4, w, False, t)
+    with pytest.raises(TypeError):
+        n.gemm_fp8_wgrad(0, 0, t, s, t, s, None, "4", w, False, t)

@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(WARPS * 32)
     for (int e = tid; e < 256; e += WARPS * 32) s_cnt[e] = 0;
     if (tid == 0) s_tokens = s_bad = 0;
     __syncthreads();
-    pdl_wait();  // the logits and ids come from the previous kernels
     pdl_trigger();
+    pdl_wait();  // the logits and ids come from the previous kernels
 
     float acc[N];
 #pragma unroll
@@ -234,8 +234,8 @@ __global__ void __launch_bounds__(256)
     __shared__ int s_tokens[8], s_bad[8], s_last;
     __shared__ double s_term[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_wait();
     pdl_trigger();
+    pdl_wait();
     const int e = blockIdx.x * kColBlock + tid % kColBlock, slice = tid / kColBlock;
     float p[PER];
     int c[PER];
@@ -333,8 +333,8 @@ __global__ void __launch_bounds__(kWarps * 32)
     float* const srow = s_row[warp][r];
     for (int c = l; c < kGroup * NV; c += kLanes) srow[c] = 0.0f;
     __syncwarp();
-    pdl_wait();
     pdl_trigger();
+    pdl_wait();
     const int E = a.E, k = a.k;
     const bool balance = a.dloss != nullptr, need_p = balance || !a.renorm;
     float f1[N], cb = 0.0f;  // f_e - 1 of this lane's columns; dloss coef / n

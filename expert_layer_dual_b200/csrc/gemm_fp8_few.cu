@@ -196,16 +196,28 @@ __global__ void __launch_bounds__(THREADS, 1)
         b->abort_flag = 0;
         fence_barrier_init();
     }
-    if (warp == MMA_WARP) tmem_alloc(&b->tmem_slot, TMEM_COLS);
+    // What does not read the operands runs while the previous kernel drains.  The next
+    // kernel may come once this one's TMEM is its own.
+    if (warp == MMA_WARP) {
+        tmem_alloc(&b->tmem_slot, TMEM_COLS);
+        pdl_trigger();
+    }
+    if (warp == A_WARP && elect_one()) tma_prefetch_desc(&tm_w);
+    if (warp == B_WARP && elect_one()) tma_prefetch_desc(&tm_x);
+    if (warp == 0 && a.offsets == nullptr) build_group_table(sm.tt, nullptr, 1, a.M, FN);
+    tc_fence_before_sync();
+    if (size > 1)
+        cluster_sync();  // every CTA's barriers exist before another arrives on them
+    else
+        __syncthreads();
+    tc_fence_after_sync();
     pdl_wait();  // the operands come from the previous kernels
-    if (warp == 0) build_group_table(sm.tt, a.offsets, a.G, a.M, FN);
     // the status word: a wait that runs out does so seconds after this store
     if (blockIdx.x == 0 && threadIdx.x == 32) *a.status = MOE_OK;
-    tc_fence_before_sync();
-    __syncthreads();
-    pdl_trigger();
-    if (size > 1) cluster_sync();  // every CTA's barriers exist before another arrives on them
-    tc_fence_after_sync();
+    if (a.offsets != nullptr) {
+        if (warp == 0) build_group_table(sm.tt, a.offsets, a.G, a.M, FN);
+        __syncthreads();
+    }
     const uint32_t tmem = b->tmem_slot;
     const int nb = a.N / 128, kbs = a.K / 128;
     const int n_tiles = INPUT ? kbs : nb;
@@ -219,7 +231,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         // ---------------------------------------------------- TMA: weights, rows
         const bool is_w = warp == A_WARP;
         const CUtensorMap* map = is_w ? &tm_w : &tm_x;
-        if (elect_one()) tma_prefetch_desc(map);
         Ring<STAGES> st;
         uint32_t issued = 0;
         bool ok = true;

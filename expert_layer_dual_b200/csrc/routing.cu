@@ -610,8 +610,8 @@ __device__ __forceinline__ void quant_row(const uint16_t* __restrict__ src, int 
 __global__ void __launch_bounds__(256)
     k_quant_act(const uint16_t* __restrict__ x, int64_t rows, int cols, uint8_t* __restrict__ q,
                 float* __restrict__ scale) {
-    pdl_wait();
     pdl_trigger();
+    pdl_wait();
     const int64_t wid = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
     const int nch = scatter_chunks(cols);
     const int64_t r = wid / nch;

@@ -1025,6 +1025,11 @@ moe_status check_product(const int32_t* offsets, int32_t G, int32_t M, int32_t N
     if (N % 128 != 0 || K % 128 != 0 || G > 256 || (int64_t)G * N >= ((int64_t)1 << 31) ||
         (int64_t)G * K >= ((int64_t)1 << 31))
         return MOE_ERR_UNSUPPORTED;
+    // tile numbers are 32 bits, in the smallest tiles (64 x 128) as in the largest
+    const int64_t wide = (N > K ? N : K) / 128;
+    if (((int64_t)M / 64 + G) * wide >= ((int64_t)1 << 31) ||
+        (int64_t)G * (N / 128) * (K / 128) >= ((int64_t)1 << 31))
+        return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 

@@ -7,6 +7,9 @@
 //   dw [n][k] = sum_b ds[b][n] xs[b][k]     sum_{m in b} dq[m][n] xq[m][k]
 // (b: blocks of 128 of the summed index).  The rows m form G groups with one
 // weight matrix each (offsets), or one group of all rows.
+#include <atomic>
+#include <mutex>
+
 #include "common.cuh"
 #include "fp8_block.cuh"
 #include "launch.h"
@@ -553,18 +556,23 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
 }
 
+// Once per device: the register split has to add up in the kernel as compiled, and
+// its shared memory is opted into.
 template <Mode MODE>
 cudaError_t set_up_once() {
-    static bool done[64] = {false};
+    static std::mutex lock;
+    static std::atomic<bool> done[64];
     const int dev = current_device_info().device;
-    if (dev < 64 && done[dev]) return cudaSuccess;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    std::lock_guard<std::mutex> hold(lock);
     cudaFuncAttributes at;
     cudaError_t e = cudaFuncGetAttributes(&at, k_product<MODE>);
     if (e != cudaSuccess) return e;
-    if (at.numRegs != REGS) return cudaErrorInvalidConfiguration;  // the split would not add up
+    if (at.numRegs != REGS) return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(k_product<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem_bytes<MODE>());
-    if (e == cudaSuccess && dev < 64) done[dev] = true;
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
     return e;
 }
 

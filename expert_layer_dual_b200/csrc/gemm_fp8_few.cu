@@ -14,6 +14,9 @@
 // With fewer tiles than SMs the blocks of the sum are split over a cluster of 2, 4
 // or 8 CTAs; each leaves its FP32 tile in its shared memory, and every CTA adds a
 // share of the rows over the cluster, in rank order (deterministic).
+#include <atomic>
+#include <mutex>
+
 #include "common.cuh"
 #include "fp8_block.cuh"
 #include "launch.h"
@@ -429,8 +432,9 @@ __global__ void __launch_bounds__(THREADS, 1)
 // The kernel's attributes, and how many clusters of 1, 2, 4 and 8 CTAs the device holds
 // at once (the GPCs' SM counts leave some idle), asked once per device.
 struct DeviceSetup {
-    bool ready;
-    int clusters[4];
+    std::mutex lock;
+    std::atomic<bool> ready{false};
+    int clusters[4] = {0, 0, 0, 0};
 };
 
 void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, uint32_t size, unsigned clusters,
@@ -450,6 +454,8 @@ void launch_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, uint32_t 
 
 template <bool INPUT>
 cudaError_t set_up(DeviceSetup* d, int num_sms) {
+    std::lock_guard<std::mutex> hold(d->lock);
+    if (d->ready.load(std::memory_order_acquire)) return cudaSuccess;
     cudaError_t e = cudaFuncSetAttribute(k_product_few<INPUT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem_bytes(true));
     if (e != cudaSuccess) return e;
@@ -463,7 +469,7 @@ cudaError_t set_up(DeviceSetup* d, int num_sms) {
         if ((e = cudaOccupancyMaxActiveClusters(&d->clusters[i], k_product_few<INPUT>, &cfg)) != cudaSuccess)
             return e;
     }
-    d->ready = true;
+    d->ready.store(true, std::memory_order_release);
     return cudaSuccess;
 }
 
@@ -473,7 +479,7 @@ cudaError_t launch(const Fp8ProductArgs& a, cudaStream_t s) {
     const DevInfo& dev = current_device_info();
     if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
     DeviceSetup& d = setups[dev.device];
-    if (!d.ready) {
+    if (!d.ready.load(std::memory_order_acquire)) {
         const cudaError_t e = set_up<INPUT>(&d, dev.num_sms);
         if (e != cudaSuccess) return e;
     }

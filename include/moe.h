@@ -526,7 +526,8 @@ moe_status moe_route_backward(const float* logits, const int32_t* ids, const flo
  * and so is the output of a group without rows.  (Offsets out of order or out of
  * range are clamped: no row outside the matrices is touched.)
  * y [M][N] of type out_type (MOE_OUT_*).  N % 128 == 0, K % 128 == 0, M >= 0,
- * 1 <= G <= 256, G*N and G*K < 2^31.  x, w, y 16-byte aligned.  ws: 256 bytes. */
+ * 1 <= G <= 256; G*N, G*K, (M/64 + G) * max(N, K)/128 and G * N/128 * K/128
+ * < 2^31.  x, w, y 16-byte aligned.  ws: 256 bytes. */
 moe_status moe_gemm_fp8(const uint8_t* x, const float* x_scale, const uint8_t* w,
                         const float* w_scale, const int32_t* offsets, int32_t G, int32_t M,
                         int32_t N, int32_t K, void* y, int32_t out_type, void* ws, size_t ws_bytes,

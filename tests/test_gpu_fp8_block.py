@@ -46,6 +46,10 @@ DENSE = [(1, 128, 128), (1, 640, 2048), (2, 256, 384), (7, 1152, 256), (16, 512,
          (33, 384, 512), (63, 256, 896), (64, 2048, 128), (65, 768, 256), (100, 384, 384), (128, 128, 256),
          (129, 256, 128), (200, 640, 640), (255, 256, 256), (256, 512, 512), (257, 384, 1152),
          (300, 1280, 256), (513, 256, 2176), (700, 896, 128), (1025, 512, 384)]
+# shapes whose 64 x 128 tiles take twice the waves of the 128 x 256 ones, so that the
+# products take the latter (forward: by N; input: the same with N and K exchanged)
+WIDE = [(1, 37120, 128), (63, 37120, 256), (130, 12800, 384), (255, 9728, 128), (257, 6400, 640), (600, 4736, 256),
+        (1500, 2176, 512), (1920, 2048, 128)]
 # (rows of each group, first row, rows behind the last group, N, K)
 GROUPED = [([5], 0, 0, 256, 128), ([0, 3, 0], 0, 0, 128, 256), ([1] * 9, 2, 5, 256, 256),
            ([130, 0, 1, 256, 77], 0, 0, 384, 256), ([0, 0], 0, 40, 128, 128), ([300, 20, 500], 7, 9, 256, 640),
@@ -82,6 +86,44 @@ def test_dense(shape, op, dtype):
     rows, N, K = shape
     got, want, size, _ = product(op, rows, N, K, 1, None, TYPES[dtype], rows + N)
     check_rows(got, want, size, (K if op == "forward" else N) // 128, TYPES[dtype])
+
+
+def takes_wide_tiles(rows, cols, groups=1, sms=148):
+    """The library's rule, for shapes that have to reach the wide tiles."""
+    avg = -(-rows // groups)
+    each = rows if groups == 1 else avg + avg // 2
+    few, wide = groups * -(-each // 64) * (cols // 128), groups * -(-each // 128) * -(-cols // 256)
+    return not -(-few // sms) < 2 * -(-wide // sms)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("op", ["forward", "input"])
+@pytest.mark.parametrize("shape", WIDE, ids=lambda s: "x".join(map(str, s)))
+def test_dense_wide(shape, op, dtype):
+    rows, cols, inner = shape
+    assert takes_wide_tiles(rows, cols)
+    N, K = (cols, inner) if op == "forward" else (inner, cols)
+    got, want, size, _ = product(op, rows, N, K, 1, None, TYPES[dtype], rows)
+    check_rows(got, want, size, inner // 128, TYPES[dtype])
+
+
+# groups for the wide tiles: empty ones, single rows, tiles filled to the row and one
+# over, a first row and rows behind
+WIDE_GROUPED = [([0, 300, 1, 0, 128, 129, 127, 700, 0], 5, 3, 5120, 256), ([256] * 6, 0, 0, 3840, 128),
+                ([1] * 40 + [900], 0, 7, 5120, 256), ([64] * 30, 0, 0, 1280, 384)]
+
+
+@pytest.mark.parametrize("op", ["forward", "input"])
+@pytest.mark.parametrize("case", range(len(WIDE_GROUPED)))
+def test_grouped_wide(case, op):
+    sizes, first, behind, cols, inner = WIDE_GROUPED[case]
+    rows, off = make_groups(sizes, first, behind)
+    assert takes_wide_tiles(rows, cols, len(sizes))
+    N, K = (cols, inner) if op == "forward" else (inner, cols)
+    for dtype in (torch.bfloat16, torch.float32):
+        got, want, size, covered = product(op, rows, N, K, len(sizes), off, dtype, case)
+        check_rows(got[covered], want[covered], size[covered], inner // 128, dtype)
+        assert bool((got[~covered] == 7.0).all())
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -201,7 +243,7 @@ def test_f16_saturates():
     assert bool((out == 65504.0).all())
 
 
-@pytest.mark.parametrize("shape", [(4, 256, 512), (400, 384, 256)])
+@pytest.mark.parametrize("shape", [(4, 256, 512), (400, 384, 256), (400, 12800, 256)])
 def test_infinite_scale_stays_in_its_row(shape):
     """A NaN code or an infinite scale reaches its own row of y only."""
     rows, N, K = shape
@@ -421,3 +463,66 @@ def test_binding_refuses_what_is_not_the_calls():
             M.gemm_fp8_wgrad(*bad)
     with pytest.raises(M.MoEError):
         M.gemm_fp8_wgrad(z(128, 0), z(0, 128, d=f32), z(256, 0), z(0, 256, d=f32), None, -1, dw, False, z(256))
+
+
+def test_unaligned_outputs_and_scales():
+    """16 bytes of alignment are enough for the outputs, 4 for the scales (the wide
+    stores and copies fall back)."""
+    def off_by(t, n):
+        flat = torch.zeros(t.numel() + 64, dtype=t.dtype, device=DEV)
+        v = flat[n: n + t.numel()].view(t.shape)
+        v.copy_(t)
+        return v
+
+    for rows, N, K in ((70, 256, 512), (600, 4736, 512)):
+        aq, a_s = [t.to(DEV) for t in ref.quantise_rows(randn((rows, K), 1))]
+        wq, ws = [t[0].to(DEV) for t in ref.quantise_weights(randn((1, N, K), 2, 0.1))]
+        for dtype, step in ((torch.bfloat16, 8), (torch.float32, 4)):
+            y = torch.empty((rows, N), dtype=dtype, device=DEV)
+            M.gemm_fp8(aq, a_s, wq, ws, None, y, workspace())
+            z = off_by(torch.zeros_like(y), step)
+            assert z.data_ptr() % 32 == 16
+            M.gemm_fp8(off_by(aq, 16), off_by(a_s, 1), off_by(wq, 16), off_by(ws, 3), None, z, workspace())
+            assert torch.equal(y, z)
+    R = M.fp8_token_rows(300, 1)
+    ops = []
+    for c, seed in ((256, 3), (384, 4)):
+        q, s = torch.empty((c, R), dtype=torch.uint8, device=DEV), torch.empty((R // 128, c), device=DEV)
+        M.quantize_fp8_tokens(randn((300, c), seed).to(DEV), None, q, s)
+        ops += [q, s]
+    dw = torch.empty((256, 384), device=DEV)
+    M.gemm_fp8_wgrad(*ops, None, 300, dw, False, workspace())
+    dz = off_by(dw * 0, 4)
+    M.gemm_fp8_wgrad(ops[0], off_by(ops[1], 1), ops[2], off_by(ops[3], 2), None, 300, dz, False, workspace())
+    assert torch.equal(dw, dz)
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first use of the products is inside a stream capture."""
+    import subprocess
+    import sys
+    code = """
+import torch, expert_layer_dual_b200.moe as M
+d = "cuda"
+z = lambda *s, t=torch.uint8: torch.full(s, 1, dtype=t, device=d)
+f = torch.float32
+a, s, w, ws, y, sp = z(40, 512), z(40, 4, t=f), z(256, 512), z(2, 4, t=f), z(40, 256, t=f), z(256)
+big, bs, bw, bws, by = z(700, 256), z(700, 2, t=f), z(4736, 256), z(37, 2, t=f), z(700, 4736, t=f)
+t, ts, dw = z(256, 128), z(1, 256, t=f), z(256, 256, t=f)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    M.gemm_fp8(a, s, w, ws, None, y, sp)
+    M.gemm_fp8(big, bs, bw, bws, None, by, sp)
+    M.gemm_fp8_wgrad(t, ts, t, ts, None, 100, dw, False, sp)
+y.zero_(), by.zero_(), dw.zero_()
+g.replay()
+torch.cuda.synchronize()
+v = 2.0 ** -9  # code 1 is the smallest e4m3 value
+assert bool((y == 512 * v * v).all()) and bool((by == 256 * v * v).all()) and bool((dw == 128 * v * v).all())
+print("fine")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]

@@ -14,13 +14,17 @@
 // near 1, and the difference of two FP32 values near 1 would keep few bits; f_e - 1
 // = (E c_e - k n) / (k n) has an exact integer numerator.
 //
-// Eight lanes hold a row, up to 32 values each in registers, so a warp works on
-// four neighbouring rows: the row sums and maxima take three exchanges for four
-// rows, and four rows' loads (up to 4 KB) are in flight per warp.  Every logit is
-// read once and every gradient written once.  With a warp per row (eight values
-// per lane, the accurate expf, the top-k part by comparing every column with
-// every id) both kernels were bound by their instructions, 210 and 496 a row: 41
-// and 82 us for 131072 rows of 256 experts, whose bytes take 20 and 41 us.
+// Sixteen lanes hold a row, up to 16 values each in registers, so a warp works on
+// two neighbouring rows: the row sums and maxima take four exchanges for two rows,
+// and a lane's values leave room for four blocks an SM, whose loads cover the
+// latency of memory.  Every logit is read once and every gradient written once, so
+// the bytes are the floor: 20 and 41 us for 131072 rows of 256 experts.  Measured
+// there: 29.7 us for the loss and 49.4 us for the gradient (4.5 and 5.4 TB/s).
+// Other splits of a row took longer: a warp per row, with the accurate expf and
+// the top-k part by comparing every column with every id, 41 and 82 us, bound by
+// its instructions (210 and 496 a row); eight lanes with 32 values each 54 and 52
+// us, bound by the few warps its registers leave.  Few tokens are bound by the
+// launches: 4.1 and 3.5 us for 64.
 //
 // Sums are FP32 within a row and over a lane's rows, FP64 over the blocks; no
 // atomic on a float, so the results do not depend on scheduling.
@@ -37,7 +41,7 @@ constexpr int kWarps = 8;                // warps per block
 constexpr int kOneWarps = 32;            // warps of the one-block kernel
 constexpr int kColBlock = 4;             // experts per block of k_balance_finish
 
-// NV: groups of 32 columns (E <= 32 NV); value 4i + c of lane l is column 32i + 4l + c.
+// NV: groups of 64 columns (E <= 64 NV); value 4i + c of lane l is column 64i + 4l + c.
 // VEC: E % 4 == 0, so the rows start on 16 bytes.
 __device__ __forceinline__ int col_of(int v, int l) { return (v >> 2) * kGroup + l * 4 + (v & 3); }
 
@@ -77,7 +81,7 @@ __device__ __forceinline__ void store_row(float* row, int E, int l, const float*
     }
 }
 
-// Over the eight lanes of a row.
+// Over the lanes of a row.
 __device__ __forceinline__ float row_max(float v) {
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -118,7 +122,7 @@ __device__ __forceinline__ double balance_fraction(int count, int E, double kn) 
 }
 
 // ---------------------------------------------------------------------------
-// Loss, first pass: a warp takes four tokens at a time and keeps the sums of its
+// Loss, first pass: a warp takes two tokens at a time and keeps the sums of its
 // tokens' probabilities in registers (a lane always holds the same columns);
 // the assignments are counted in shared memory (integers).  The block's sums go
 // to its row of the partials.  ONE: a single block, which finishes the result
@@ -166,7 +170,7 @@ __global__ void __launch_bounds__(WARPS * 32)
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
     }
-    // the warp's four rows, then the block's warps
+    // the warp's two rows, then the block's warps
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         for (int o = kLanes; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------------------
-// Gradient of the logits: four rows per warp as above, the softmax recomputed
+// Gradient of the logits: two rows per warp as above, the softmax recomputed
 // from the logits (nothing more is read).  The k values of the top-k part go to
 // their columns through a row of shared memory that is zero in between; ids that
 // repeat within a row are added up first, so their order does not matter.
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
 }
 
-// The instance for E experts: groups of 32 columns rounded up to 1, 2, 4 or 8.
+// The instance for E experts: groups of 64 columns, rounded up to 1, 2 or 4.
 template <typename F>
 cudaError_t by_width(int E, F f) {
     const bool vec = E % 4 == 0;

@@ -140,7 +140,6 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-
 __device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
@@ -249,7 +248,7 @@ __device__ __forceinline__ bool aligned16(const void* p) {
 }
 
 // ---------------------------------------------------------------- e4m3 codes of a group
-// s = fp32(amax) / 448 (1 for a group of zeros), rounded as the IEEE division: the
+// s = fp32(amax) / 448 (1 for a group of zeros, or of NaN only), rounded as the IEEE division: the
 // product with 1/448 corrected by one FMA residual, which is the rounded
 // quotient where nothing underflows or overflows on the way (every bf16 amax is
 // tested), else the division.
@@ -259,7 +258,7 @@ __device__ __forceinline__ float block_scale(float amax) {
         const float q = amax * r;
         return fmaf(fmaf(-448.0f, q, amax), r, q);
     }
-    return amax == 0.0f ? 1.0f : __fdiv_rn(amax, 448.0f);
+    return amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
 }
 
 // Codes e4m3(fp32(v / s)) of bf16 values, rounded to nearest even and saturating,
@@ -269,10 +268,11 @@ __device__ __forceinline__ float block_scale(float amax) {
 // the reciprocal is rounded (1 ulp; all 3 * 128 * 128 cases are tested), as long
 // as nothing underflows; below 2^-100 the code is a zero either way.  Scales near
 // the ends of the FP32 range divide.  The correction turns -0 into +0, so the
-// codes take their signs from the values.
+// codes take their signs from the values; NaN has the code 0x7F whatever its sign.
 // (Bracketing the quotient between two roundings and dividing where they differ
 // was slower: bf16 values over a bf16 maximum meet exact ties in a group out of
-// seven.  8192 x 6144 values: 38 us so, and 41 with divisions.)
+// seven.  8192 x 6144 values: 38 us so, 41 with divisions, 30.6 with the
+// correction.)
 struct GroupQuotient {
     float s, r;  // r = 0: divide
     __device__ __forceinline__ GroupQuotient(float scale, float reciprocal) : s(scale), r(reciprocal) {}
@@ -300,7 +300,9 @@ struct GroupQuotient {
     }
     // codes of four values; `signs` holds a value's sign in bit 7 of each byte
     __device__ __forceinline__ uint32_t codes4(uint64_t p0, uint64_t p1, uint32_t signs) const {
-        return cvt(quotient(p0)) | cvt(quotient(p1)) << 16 | (signs & 0x80808080u);
+        const uint32_t c = cvt(quotient(p0)) | cvt(quotient(p1)) << 16;
+        const uint32_t nan = (c & 0x7F7F7F7Fu) + 0x01010101u;  // bit 7 of each byte
+        return c | (signs & ~nan & 0x80808080u);
     }
 };
 

@@ -321,14 +321,24 @@ __device__ __forceinline__ void store_tile(const Fp8ProductArgs& a, int64_t row0
 // epilogue warps take each partial out of TMEM and add it, scaled, to FP32
 // accumulators in registers while the next block's MMAs run.
 //
-// Sixteen epilogue warps of 64 accumulators take a 128 x 256 partial out in ~280
-// cycles (2 x 32-column loads each; 480 with spilled registers), below the 512 of
-// its MMAs.  What is left of a block's time is the way round: commit, wait, the
-// TMEM loads, the arrival, the next issue (with both TMEM halves in use ~880
-// cycles per block).  On CTA pairs (M = 256, the operands' shared-memory traffic
-// a third less) the longer way round through the other CTA's barriers took what
-// the rate gave: 187 us for 8192 x 4096 x 6144 both ways, and ragged groups lost
-// to the 256-row tiles (290 against 275 us); so one CTA per tile.
+// Bound: the tensor cores' 512 cycles a block (4 MMAs of 128), and the way round:
+// commit, wait, TMEM loads, products, arrival, next issue.  Cycles per block of a
+// 128 x 256 tile: 815 in all, 720 without the MMAs, 613 without the promotion,
+// 520 with neither.  At large sizes the power limit levels what is left of the
+// difference: 8192 x 4096 x 6144 takes 182 us (2.26 PFLOP/s) at ~1.5 GHz, 143 us
+// without its promotion, and variants with 5% fewer cycles took the same 182 us
+// at a lower clock.  The weight gradient (two products a value) takes 295 us,
+// 4096 x 6144 x 2048 rows of the input gradient 52 us, 32 groups of 8192 rows 280
+// us (their 805 MB of weights alone 123 us; the groups' last tiles pad 336
+// tiles of rows to 432).
+//
+// Sixteen epilogue warps of 64 accumulators each fit without spills (480 cycles of
+// promotion with spilled registers, so 256).  On CTA pairs (M = 256, the operands'
+// shared-memory traffic a third less) the longer way round through the other
+// CTA's barriers took what the rate gave: 187 against 185 us for 8192 x 4096 x 6144,
+// and ragged groups lost to the 256-row tiles (290 against 275 us); so one CTA per
+// tile.  128 x 128 tiles with four partials took 14% more cycles (weight gradient);
+// two halves of the epilogue warps a partial apart, 4 to 12% more.
 // ---------------------------------------------------------------------------
 template <Mode MODE>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -614,7 +624,8 @@ cudaError_t launch_tiles(const Fp8ProductArgs& a, cudaStream_t s) {
 // threads takes 128 tokens x 64 columns: 16-byte loads, the column maxima by
 // shuffles and shared memory, and the codes turned in shared memory so that
 // each column's 128 codes leave as one 128-byte run.  2 bytes are read and 1
-// written per value.
+// written per value: 8192 x 6144 values take 32.5 us (4.65 TB/s; 47 us with an
+// IEEE division per value, which bound it).
 // ---------------------------------------------------------------------------
 constexpr int QC = 64;
 

@@ -14,6 +14,12 @@
 // With fewer tiles than SMs the blocks of the sum are split over a cluster of 2, 4
 // or 8 CTAs; each leaves its FP32 tile in its shared memory, and every CTA adds a
 // share of the rows over the cluster, in rank order (deterministic).
+//
+// Measured: 1 x 6144 x 2048 6.2 us, 1 x 4096 x 6144 7.8 us (the 128 x 256 tiles 23.5),
+// 64 x 4096 x 6144 9.8 us, the input gradient 64 x 6144 x 2048 8.7 us, and 1 x 8192 x
+// 8192 15.0 us (67 MB, 4.5 TB/s).  At the small sizes the weights' bytes would
+// take 2 to 4 us: the rest is the launch, the first load's latency and the
+// cluster's exchange.
 #include <atomic>
 #include <mutex>
 

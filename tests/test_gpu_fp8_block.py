@@ -432,6 +432,31 @@ def test_scale_of_every_bf16_maximum():
     assert torch.equal(s.cpu(), ws) and torch.equal(q.cpu(), wq)
 
 
+def test_codes_of_values_that_are_not_finite():
+    """NaN and infinities in a group: the codes and scales are those of the quantiser
+    of permuted rows (here in the rows' own order), which divides, and the same
+    along the tokens."""
+    bf = torch.bfloat16
+    rows = []
+    for special in ([float("nan")], [float("inf")], [-float("inf")], [float("nan"), -float("inf")],
+                    [-0.0, float("nan")]):
+        for n in (1, 5, 128):
+            r = torch.linspace(-3, 3, 128).to(bf)
+            v = torch.tensor(special).to(bf)
+            r[:n] = v.repeat(128)[:n]
+            rows += [r, (r.view(torch.int16) ^ -32768).view(bf)]   # the signs of NaN too
+    x = torch.stack(rows)
+    x = torch.cat([x, x[: 128 % x.shape[0]], x, x, x])[:128].contiguous()
+    T = x.shape[0]
+    q, pq, qt = (torch.empty((T, 128), dtype=torch.uint8, device=DEV) for _ in range(3))
+    s, ps, st = (torch.empty((T, 1), device=DEV) for _ in range(3))
+    M.quantize_act_fp8(x.to(DEV), q, s)
+    M.quantize_act_fp8_permuted(x.to(DEV), torch.arange(T, dtype=torch.int32, device=DEV), 1, 0, pq, ps)
+    assert torch.equal(q, pq) and torch.equal(s.view(torch.int32), ps.view(torch.int32))
+    M.quantize_fp8_tokens(x.T.contiguous().to(DEV), None, qt, st.T)
+    assert torch.equal(qt, pq) and torch.equal(st.view(torch.int32), ps.view(torch.int32))
+
+
 def test_binding_refuses_what_is_not_the_calls():
     """Shapes, types, layouts and devices that do not fit raise ValueError before a
     launch; limits of the library come back as its status."""

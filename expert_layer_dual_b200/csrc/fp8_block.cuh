@@ -89,6 +89,11 @@ __device__ __forceinline__ float4 lds4(uint32_t a) {
                  : "r"(a));
     return v;
 }
+__device__ __forceinline__ uint64_t lds2(uint32_t a) {  // a pair for the packed products
+    uint64_t v;
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(a));
+    return v;
+}
 __device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
@@ -225,10 +230,12 @@ __device__ __forceinline__ void tmem_arrived(uint32_t* r) {
                  :
                  : "memory");
 }
-// The same for 16 columns.
+// 32 FP32 columns of 16 TMEM lanes, shared out over rows and columns: of the columns
+// 8g .. 8g + 7, r[4g] and r[4g + 1] are columns 2 (l % 4) and the next of TMEM lane
+// l / 4 (l: this thread's lane), r[4g + 2] and r[4g + 3] of TMEM lane l / 4 + 8.
 __device__ __forceinline__ void tmem_fetch16(uint32_t taddr, uint32_t* r) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : W4(r, 0), W4(r, 4), W4(r, 8), W4(r, 12)
         : "r"(taddr)

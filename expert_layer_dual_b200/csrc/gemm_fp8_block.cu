@@ -209,25 +209,27 @@ __device__ __forceinline__ void promote(const uint32_t* r, uint64_t ff, uint64_t
     for (int i = 0; i < COLS / 2; ++i)
         acc[i] = f32x2_fma(ff, f32x2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), acc[i]);
 }
-// The same with column scales (floats at shared address cs): f * (cs * P).
-template <int COLS>
-__device__ __forceinline__ void promote_scaled(const uint32_t* r, uint64_t ff, uint32_t cs, uint64_t* acc) {
+// The same with column scales, for what tmem_fetch16 brings: f of rows l / 4 and l / 4
+// + 8, c the scales of this thread's columns.
+__device__ __forceinline__ void promote_scaled(const uint32_t* r, float f0, float f1, const uint64_t* c,
+                                               uint64_t* acc0, uint64_t* acc1) {
+    const uint64_t ff0 = f32x2_pack(f0, f0), ff1 = f32x2_pack(f1, f1);
 #pragma unroll
-    for (int i = 0; i < COLS / 2; i += 2) {
-        const float4 s = lds4(cs + 8 * i);
-        const uint64_t p0 = f32x2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-        const uint64_t p1 = f32x2_pack(__uint_as_float(r[2 * i + 2]), __uint_as_float(r[2 * i + 3]));
-        acc[i] = f32x2_fma(ff, f32x2_mul(p0, f32x2_pack(s.x, s.y)), acc[i]);
-        acc[i + 1] = f32x2_fma(ff, f32x2_mul(p1, f32x2_pack(s.z, s.w)), acc[i + 1]);
+    for (int g = 0; g < 4; ++g) {
+        const uint64_t p0 = f32x2_pack(__uint_as_float(r[4 * g]), __uint_as_float(r[4 * g + 1]));
+        const uint64_t p1 = f32x2_pack(__uint_as_float(r[4 * g + 2]), __uint_as_float(r[4 * g + 3]));
+        acc0[g] = f32x2_fma(ff0, f32x2_mul(p0, c[g]), acc0[g]);
+        acc1[g] = f32x2_fma(ff1, f32x2_mul(p1, c[g]), acc1[g]);
     }
 }
 
-// Four chunks of eight words in each of four neighbouring lanes, turned: lane j of the
+// Four chunks of W words in each of four neighbouring lanes, turned: lane j of the
 // four ends with chunk j of all four lanes, in lane order.  The accumulators hold
 // a row per lane; turned, the four lanes store 128 consecutive bytes of one row
 // at a time.  (A store of 32 bytes from each of 32 rows kept the store unit four
 // times as long: the weight gradients of 32 small experts, 369 MB, took
 // 103 us, so 85.)
+template <int W>
 __device__ __forceinline__ void turn_chunks(uint32_t* v) {
     const int j = threadIdx.x & 3;
 #pragma unroll
@@ -237,8 +239,8 @@ __device__ __forceinline__ void turn_chunks(uint32_t* v) {
         for (int k = 0; k < 4; ++k) {
             if (k & step) continue;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) {
-                uint32_t &lo = v[8 * k + w], &hi = v[8 * (k + step) + w];
+            for (int w = 0; w < W; ++w) {
+                uint32_t &lo = v[W * k + w], &hi = v[W * (k + step) + w];
                 const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, step);
                 if (up) lo = got; else hi = got;
             }
@@ -265,7 +267,35 @@ __device__ __forceinline__ void store_tile(const Fp8ProductArgs& a, int64_t row0
                                            const uint64_t* acc) {
     static_assert(EPI_COLS == 64, "two halves of 32 words, or one of 32 pairs");
     const int lane = threadIdx.x & 31, first = lane & ~3, j = lane & 3;
-    if (MODE == kWeight || a.out_type == MOE_OUT_F32) {
+    if (MODE == kWeight) {
+        // rows l / 4 + 8 q, of each eight columns a pair: turned, eight columns of each 32
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[8];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    float lo, hi;
+                    f32x2_unpack(acc[8 * q + 4 * h + g], lo, hi);
+                    w[2 * g] = __float_as_uint(lo);
+                    w[2 * g + 1] = __float_as_uint(hi);
+                }
+                turn_chunks<2>(w);
+                float* dst = static_cast<float*>(a.out) + (row0 + 8 * q + (lane >> 2)) * cols + col + 32 * h + 8 * j;
+                if (a.accumulate) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 o = *reinterpret_cast<const float4*>(dst + 4 * i);
+                        w[4 * i] = __float_as_uint(__uint_as_float(w[4 * i]) + o.x);
+                        w[4 * i + 1] = __float_as_uint(__uint_as_float(w[4 * i + 1]) + o.y);
+                        w[4 * i + 2] = __float_as_uint(__uint_as_float(w[4 * i + 2]) + o.z);
+                        w[4 * i + 3] = __float_as_uint(__uint_as_float(w[4 * i + 3]) + o.w);
+                    }
+                }
+                store8(reinterpret_cast<uint32_t*>(dst), w);
+            }
+    } else if (a.out_type == MOE_OUT_F32) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t w[32];
@@ -276,22 +306,11 @@ __device__ __forceinline__ void store_tile(const Fp8ProductArgs& a, int64_t row0
                 w[2 * i] = __float_as_uint(lo);
                 w[2 * i + 1] = __float_as_uint(hi);
             }
-            turn_chunks(w);
+            turn_chunks<8>(w);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (first + i >= valid) break;
                 float* dst = static_cast<float*>(a.out) + (row0 + first + i) * cols + col + 32 * h + 8 * j;
-                if (MODE == kWeight && a.accumulate) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float4 o = *reinterpret_cast<const float4*>(dst + 4 * q);
-                        uint32_t* v = w + 8 * i + 4 * q;
-                        v[0] = __float_as_uint(__uint_as_float(v[0]) + o.x);
-                        v[1] = __float_as_uint(__uint_as_float(v[1]) + o.y);
-                        v[2] = __float_as_uint(__uint_as_float(v[2]) + o.z);
-                        v[3] = __float_as_uint(__uint_as_float(v[3]) + o.w);
-                    }
-                }
                 store8(reinterpret_cast<uint32_t*>(dst), w + 8 * i);
             }
         }
@@ -304,7 +323,7 @@ __device__ __forceinline__ void store_tile(const Fp8ProductArgs& a, int64_t row0
             f32x2_unpack(acc[i], lo, hi);
             w[i] = f16 ? pack_f16x2_sat(lo, hi) : pack_bf16x2(lo, hi);
         }
-        turn_chunks(w);
+        turn_chunks<8>(w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (first + i >= valid) break;
@@ -325,9 +344,9 @@ __device__ __forceinline__ void store_tile(const Fp8ProductArgs& a, int64_t row0
 // commit, wait, TMEM loads, products, arrival, next issue.  Cycles per block of a
 // 128 x 256 tile: 815 in all, 720 without the MMAs, 613 without the promotion,
 // 520 with neither.  At large sizes the power limit levels what is left of the
-// difference: 8192 x 4096 x 6144 takes 182 us (2.26 PFLOP/s) at ~1.5 GHz, 143 us
-// without its promotion, and variants with 5% fewer cycles took the same 182 us
-// at a lower clock.  The weight gradient (two products a value) takes 295 us,
+// difference: 8192 x 4096 x 6144 takes 180 us (2.29 PFLOP/s) at ~1.5 GHz, 143 us
+// without its promotion, and variants with 5% fewer cycles took the same time
+// at a lower clock.  The weight gradient (two products a value) takes 260 us,
 // 4096 x 6144 x 2048 rows of the input gradient 52 us, 32 groups of 8192 rows 280
 // us (their 805 MB of weights alone 123 us; the groups' last tiles pad 336
 // tiles of rows to 432).
@@ -486,62 +505,81 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int j = 0; j < EPI_COLS / 2; ++j) acc[j] = 0ull;
 #pragma unroll 1
-            for (int kb = 0; kb < blocks; ++kb) {
-                const int kk = kb % SC_KB;
-                if (kk == 0 && !warp_wait_phase(sm.sfull(ch.slot), ch.round, a.timeout_ns, sm.abort_flag())) {
+            for (int k0 = 0; ok && k0 < blocks; k0 += SC_KB, ch.next()) {
+                if (!warp_wait_phase(sm.sfull(ch.slot), ch.round, a.timeout_ns, sm.abort_flag())) {
                     ok = false;
                     break;
                 }
                 const uint32_t sc = sm.scales + 4u * ch.slot * SL::CHUNK;
-                float f = lds(sc + 4u * (CS ? kk * BM + row : row * SC_KB + kk));
-                if (!CS) f *= lds(sc + 4u * (SL::COLS + kk * 4 + part * EPI_COLS / 128));
-                const uint64_t ff = f32x2_pack(f, f);
-                const uint32_t cs = sc + 4u * (SL::COLS + kk * BN + part * EPI_COLS);
-                if (!warp_wait_phase(sm.done(st.slot), st.round, a.timeout_ns, sm.abort_flag())) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after_sync();
-                const uint32_t p = taddr + pb * BN;
-                auto release = [&] {  // the partial is in registers
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (elect_one()) arrive(sm.pempty(pb));
-                };
-                if constexpr (CS) {
-                    // sixteen columns in flight over the products of sixteen others: with
-                    // two products a value the loads would wait behind 32 (315 against
-                    // 295 us, 8192 rows x 4096 x 6144)
-                    uint32_t r[2][16];
-                    tmem_fetch16(p, r[0]);
+                const int n = min(SC_KB, blocks - k0);
+#pragma unroll 1
+                for (int kk = 0; kk < n; ++kk) {
+                    float f[CS ? 4 : 1];  // CS: of rows lane / 4 + 8 q
+                    if (CS) {
 #pragma unroll
-                    for (int q = 0; q < EPI_COLS / 16; ++q) {
-                        tmem_arrived16(r[q & 1]);
-                        if (q + 1 < EPI_COLS / 16)
-                            tmem_fetch16(p + 16 * (q + 1), r[(q + 1) & 1]);
-                        else
-                            release();
-                        promote_scaled<16>(r[q & 1], ff, cs + 64 * q, acc + 8 * q);
+                        for (int q = 0; q < 4; ++q) f[q] = lds(sc + 4u * (kk * BM + quad * 32 + 8 * q + (lane >> 2)));
+                    } else {
+                        f[0] = lds(sc + 4u * (row * SC_KB + kk)) *
+                               lds(sc + 4u * (SL::COLS + kk * 4 + part * EPI_COLS / 128));
                     }
-                } else {
-                    // 32 at a time, the other warps' products over the loads (in halves
-                    // of 16 as above 235 against 182 us, 8192 x 4096 x 6144)
-                    uint32_t r[32];
+                    const uint32_t cs = sc + 4u * (SL::COLS + kk * BN + part * EPI_COLS + 2 * (lane & 3));
+                    uint64_t c[4];  // CS: the scales of half this thread's columns
+                    if (CS) {
 #pragma unroll
-                    for (int q = 0; q < EPI_COLS / 32; ++q) {
-                        tmem_fetch32(p + 32 * q, r);
-                        tmem_arrived(r);
-                        if (q == EPI_COLS / 32 - 1) release();
-                        promote<32>(r, ff, acc + 16 * q);
+                        for (int g = 0; g < 4; ++g) c[g] = lds2(cs + 32 * g);
                     }
+                    if (!warp_wait_phase(sm.done(st.slot), st.round, a.timeout_ns, sm.abort_flag())) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t p = taddr + pb * BN;
+                    auto release = [&] {  // the partial is in registers
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (elect_one()) arrive(sm.pempty(pb));
+                    };
+                    if constexpr (CS) {
+                        // Four rows of sixteen columns a thread: with a row a thread, every
+                        // thread would read all of its 64 columns' scales, 131 KB a block, more
+                        // than shared memory gives in the block's time (298 against 274 us,
+                        // 8192 rows x 4096 x 6144).  A quarter in flight over the products of
+                        // another, the next scales ahead of the wait (274 against 260).
+                        uint32_t r[2][16];
+                        tmem_fetch16(p, r[0]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {  // rows of the lower and the upper half by turns
+                            tmem_arrived16(r[q & 1]);
+                            if (q + 1 < 4)
+                                tmem_fetch16(p + ((q + 1) & 1) * (16u << 16) + ((q + 1) >> 1) * 32, r[(q + 1) & 1]);
+                            else
+                                release();
+                            const int h = q & 1, k = q >> 1;
+                            promote_scaled(r[h], f[2 * h], f[2 * h + 1], c, acc + 16 * h + 4 * k,
+                                           acc + 16 * h + 8 + 4 * k);
+                            if (q == 1) {
+#pragma unroll
+                                for (int g = 0; g < 4; ++g) c[g] = lds2(cs + 128 + 32 * g);
+                            }
+                        }
+                    } else {
+                        // 32 at a time, the other warps' products over the loads (16 in flight
+                        // over 16 as above 235 against 182 us, 8192 x 4096 x 6144)
+                        const uint64_t ff = f32x2_pack(f[0], f[0]);
+                        uint32_t r[32];
+#pragma unroll
+                        for (int q = 0; q < EPI_COLS / 32; ++q) {
+                            tmem_fetch32(p + 32 * q, r);
+                            tmem_arrived(r);
+                            if (q == EPI_COLS / 32 - 1) release();
+                            promote<32>(r, ff, acc + 16 * q);
+                        }
+                    }
+                    st.next();
+                    pb ^= 1u;
                 }
-                st.next();
-                pb ^= 1u;
-                if (kk == SC_KB - 1 || kb == blocks - 1) {
-                    __syncwarp();
-                    if (elect_one()) arrive(sm.sempty(ch.slot));
-                    ch.next();
-                }
+                __syncwarp();
+                if (ok && elect_one()) arrive(sm.sempty(ch.slot));
             }
             if (!ok) {
                 if (lane == 0) fail(sm, a.status);

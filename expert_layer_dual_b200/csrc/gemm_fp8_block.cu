@@ -79,15 +79,17 @@ __device__ __forceinline__ void fail(const Smem& sm, int32_t* status) {
 
 // ---------------------------------------------------------------- tiles
 // One tile: rows row0 .. (nrows <= 128) and columns col0 .. (256) of the output, group
-// g, and the scale blocks [block0, block0 + blocks) that it sums over (kWeight:
-// token blocks of the group; else all of them, from 0).
+// g, and the scale blocks [block0, block0 + blocks) that this CTA sums over (kWeight:
+// token blocks of the group; else all of them, from 0), or its share of them.
 struct PTile {
     int g, row0, nrows, col0, block0, blocks;
 };
 
-template <Mode MODE>
+// SPLIT: a cluster of a.split CTAs works on each tile, CTA `rank` on its share of the
+// blocks (four at a time, as the scales are read).
+template <Mode MODE, bool SPLIT>
 struct Work {
-    int total, n_tiles, k_tiles, blocks;
+    int total, n_tiles, k_tiles, blocks, first, step;
     __device__ __forceinline__ Work(const Fp8ProductArgs& a, const TileTable* tt) {
         if (MODE == kWeight) {
             n_tiles = (a.K + BN - 1) / BN;
@@ -98,6 +100,8 @@ struct Work {
             blocks = (MODE == kForward ? a.K : a.N) / BK;
             total = tt->mstart[a.G] * n_tiles;
         }
+        first = SPLIT ? blockIdx.x / a.split : blockIdx.x;
+        step = SPLIT ? gridDim.x / a.split : gridDim.x;
     }
     __device__ __forceinline__ PTile tile(const Fp8ProductArgs& a, const TileTable* tt, int i) const {
         PTile p;
@@ -119,6 +123,12 @@ struct Work {
             p.block0 = 0;
             p.blocks = blocks;
         }
+        if (SPLIT) {
+            const int size = a.split, per = ((p.blocks + size - 1) / size + SC_KB - 1) / SC_KB * SC_KB;
+            const int lo = min(p.blocks, (int)(blockIdx.x % size) * per);
+            p.block0 += lo;
+            p.blocks = min(p.blocks - lo, per);
+        }
         return p;
     }
 };
@@ -130,8 +140,8 @@ struct Work {
 // four columns, side by side and aligned), else 4-byte ones.  Rows and columns
 // past the tile read a neighbour's scale or, past the matrix, the last one: what
 // they scale is not stored.
-template <Mode MODE>
-__device__ __forceinline__ void scale_role(const Fp8ProductArgs& a, const Smem& sm, const Work<MODE>& work) {
+template <Mode MODE, bool SPLIT>
+__device__ __forceinline__ void scale_role(const Fp8ProductArgs& a, const Smem& sm, const Work<MODE, SPLIT>& work) {
     using SL = ScaleLayout<MODE>;
     const int lane = threadIdx.x & 31;
     const int nb = a.N / 128, kbs = a.K / 128;
@@ -140,7 +150,7 @@ __device__ __forceinline__ void scale_role(const Fp8ProductArgs& a, const Smem& 
                                       : aligned16(a.a_scale) && per_row % 4 == 0;
     Ring<SC_BUFS> ring;
     bool ok = true;
-    for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
+    for (int i = work.first; ok && i < work.total; i += work.step) {
         const PTile t = work.tile(a, sm.tt, i);
         for (int k0 = 0; k0 < t.blocks; k0 += SC_KB, ring.next()) {
             if (!warp_wait_phase(sm.sempty(ring.slot), ring.round ^ 1u, a.timeout_ns, sm.abort_flag())) {
@@ -173,7 +183,8 @@ __device__ __forceinline__ void scale_role(const Fp8ProductArgs& a, const Smem& 
             } else {
 #pragma unroll 1
                 for (int r = lane; r < BM; r += 32) {
-                    const float* src = a.a_scale + (int64_t)min(t.row0 + r, a.M - 1) * per_row + k0;
+                    const float* src =
+                        a.a_scale + (int64_t)min(t.row0 + r, a.M - 1) * per_row + t.block0 + k0;
                     const uint32_t d = dst + 16u * r;
                     if (wide) {
                         cp_async_16(d, src, 16u);
@@ -187,8 +198,8 @@ __device__ __forceinline__ void scale_role(const Fp8ProductArgs& a, const Smem& 
                     const int last = (MODE == kForward ? nb : kbs) - 1;
                     const int col = min(t.col0 / 128 + c, last);
                     const int64_t at = (int64_t)t.g * nb * kbs +
-                                       (MODE == kForward ? (int64_t)col * kbs + k0 + kk
-                                                         : (int64_t)(k0 + kk) * kbs + col);
+                                       (MODE == kForward ? (int64_t)col * kbs + t.block0 + k0 + kk
+                                                         : (int64_t)(t.block0 + k0 + kk) * kbs + col);
                     cp_async_4(dst + 4u * (SL::COLS + kk * 4 + c), a.b_scale + at, 4u);
                 }
             }
@@ -333,6 +344,93 @@ __device__ __forceinline__ void store_tile(const Fp8ProductArgs& a, int64_t row0
     }
 }
 
+// A tile split over a cluster: every CTA leaves its sums in its shared memory (where
+// the operands were: every MMA that read them is complete), and adds its share of
+// the rows over the CTAs, in rank order.
+constexpr int LEFT_COLS = BN + 8;  // of a row: eight rows' pairs, or quarters, on distinct banks
+static_assert(BM * LEFT_COLS * 4 <= STAGES * STAGE_BYTES, "the tile fits where the operands were");
+
+template <Mode MODE>
+__device__ __forceinline__ void leave_tile(const Smem& sm, int quad, int part, int lane, const uint64_t* acc) {
+    if (MODE == kWeight) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                const int at = (quad * 32 + 8 * q + (lane >> 2)) * LEFT_COLS + part * EPI_COLS + 8 * g + 2 * (lane & 3);
+                asm volatile("st.shared.b64 [%0], %1;" ::"r"(sm.stages + 4u * at), "l"(acc[8 * q + g]) : "memory");
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPI_COLS / 4; ++i) {
+            const int at = (quad * 32 + lane) * LEFT_COLS + part * EPI_COLS + 4 * i;
+            asm volatile("st.shared.v2.b64 [%0], {%1, %2};" ::"r"(sm.stages + 4u * at), "l"(acc[2 * i]),
+                         "l"(acc[2 * i + 1])
+                         : "memory");
+        }
+    }
+}
+
+template <Mode MODE, int SIZE>
+__device__ __forceinline__ void add_tiles(const Fp8ProductArgs& a, const Smem& sm, const PTile& t, int warp,
+                                          int lane) {
+    const int rank = blockIdx.x % SIZE, cols = MODE == kForward ? a.N : a.K, col = t.col0 + 8 * lane;
+    if (col >= cols) return;
+    // nothing to add to a group without rows
+    if (MODE == kWeight && a.accumulate && sm.tt->mstart[t.g] == sm.tt->mstart[t.g + 1]) return;
+    const int64_t row0 = MODE == kWeight ? (int64_t)t.g * a.N + t.row0 : t.row0;
+    uint32_t from[SIZE];
+#pragma unroll
+    for (int c = 0; c < SIZE; ++c)
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from[c]) : "r"(sm.stages + 32u * lane), "r"(c));
+#pragma unroll 1
+    for (int r = rank * (BM / SIZE) + warp; r < (rank + 1) * (BM / SIZE); r += EPI_WARPS) {
+        if (r >= t.nrows) break;
+        float s[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float4 v[SIZE];
+#pragma unroll
+            for (int c = 0; c < SIZE; ++c)
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(v[c].x), "=f"(v[c].y), "=f"(v[c].z), "=f"(v[c].w)
+                             : "r"(from[c] + 4u * r * LEFT_COLS + 16u * h)
+                             : "memory");
+            float4 u = v[0];
+#pragma unroll
+            for (int c = 1; c < SIZE; ++c) {
+                u.x += v[c].x;
+                u.y += v[c].y;
+                u.z += v[c].z;
+                u.w += v[c].w;
+            }
+            s[4 * h] = u.x;
+            s[4 * h + 1] = u.y;
+            s[4 * h + 2] = u.z;
+            s[4 * h + 3] = u.w;
+        }
+        const int64_t at = (row0 + r) * cols + col;
+        if (MODE == kWeight || a.out_type == MOE_OUT_F32) {
+            float* dst = static_cast<float*>(a.out) + at;
+            if (MODE == kWeight && a.accumulate) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i] += dst[i];
+            }
+            st_global_v4(dst, __float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]),
+                         __float_as_uint(s[3]));
+            st_global_v4(dst + 4, __float_as_uint(s[4]), __float_as_uint(s[5]), __float_as_uint(s[6]),
+                         __float_as_uint(s[7]));
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = a.out_type == MOE_OUT_F16 ? pack_f16x2_sat(s[2 * i], s[2 * i + 1])
+                                                 : pack_bf16x2(s[2 * i], s[2 * i + 1]);
+            st_global_v4(static_cast<uint16_t*>(a.out) + at, w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------
 // The product.  Per scale block of the summed index one warp issues four M = 128,
 // N = 256, K = 32 MMAs into a fresh partial (one of two in TMEM) and one commit,
@@ -359,7 +457,7 @@ __device__ __forceinline__ void store_tile(const Fp8ProductArgs& a, int64_t row0
 // tile.  128 x 128 tiles with four partials took 14% more cycles (weight gradient);
 // two halves of the epilogue warps a partial apart, 4 to 12% more.
 // ---------------------------------------------------------------------------
-template <Mode MODE>
+template <Mode MODE, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
     k_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                    const __grid_constant__ Fp8ProductArgs a) {
@@ -402,7 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = b->tmem_slot;
-    const Work<MODE> work(a, sm.tt);
+    const Work<MODE, SPLIT> work(a, sm.tt);
 
     if (warp >= EPI_WARPS) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_HELP));
@@ -414,18 +512,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             Ring<STAGES> st;
             uint32_t issued = 0;
             bool ok = true;
-            for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
+            for (int i = work.first; ok && i < work.total; i += work.step) {
                 const PTile t = work.tile(a, sm.tt, i);
                 int x, y;  // of the tile's first block
                 if (is_a) {
                     x = t.block0 * BK;
                     y = t.row0;
                 } else if (MODE == kForward) {
-                    x = 0;
+                    x = t.block0 * BK;
                     y = t.g * a.N + t.col0;
                 } else if (MODE == kInput) {
                     x = t.col0;
-                    y = t.g * a.N;
+                    y = t.g * a.N + t.block0 * BK;
                 } else {
                     x = t.block0 * BK;
                     y = t.col0;
@@ -458,7 +556,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             Ring<STAGES> st;
             Ring<NPART> pt;
             bool ok = true;
-            for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
+            for (int i = work.first; ok && i < work.total; i += work.step) {
                 const int blocks = work.tile(a, sm.tt, i).blocks;
                 for (int kb = 0; kb < blocks; ++kb, st.next(), pt.next()) {
                     if (!warp_wait_phase(sm.full(st.slot), st.round, a.timeout_ns, sm.abort_flag()) ||
@@ -485,9 +583,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (!ok && lane == 0) fail(sm, a.status);
         } else {
             // ------------------------------------------------ scales, SC_KB blocks at a time
-            scale_role<MODE>(a, sm, work);
+            scale_role<MODE, SPLIT>(a, sm, work);
         }
         __syncwarp();
+        if (SPLIT) cluster_sync();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
         // ---------------------------------------------------- promotion and output
@@ -499,7 +598,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         Ring<SC_BUFS> ch;
         uint32_t pb = 0;
         bool ok = true;
-        for (int i = blockIdx.x; ok && i < work.total; i += gridDim.x) {
+        for (int i = work.first; ok && i < work.total; i += work.step) {
             const int blocks = work.tile(a, sm.tt, i).blocks;
             uint64_t acc[EPI_COLS / 2];
 #pragma unroll
@@ -585,6 +684,10 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (lane == 0) fail(sm, a.status);
                 break;
             }
+            if constexpr (SPLIT) {  // the only tile
+                leave_tile<MODE>(sm, quad, part, lane, acc);
+                break;
+            }
             // decoded again rather than kept: the loop has no registers to spare
             const PTile t = work.tile(a, sm.tt, i);
             const int cols = MODE == kForward ? a.N : a.K;
@@ -595,40 +698,85 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             __syncwarp();
         }
+        if constexpr (SPLIT) {
+            __syncwarp();
+            cluster_sync();  // every CTA's tile is in its shared memory
+            const PTile t = work.tile(a, sm.tt, work.first);
+            switch (a.split) {
+                case 2: add_tiles<MODE, 2>(a, sm, t, warp, lane); break;
+                case 4: add_tiles<MODE, 4>(a, sm, t, warp, lane); break;
+                default: add_tiles<MODE, 8>(a, sm, t, warp, lane); break;
+            }
+        }
     }
+    __syncwarp();
     tc_fence_before_sync();
-    __syncthreads();
+    if (SPLIT) {
+        cluster_sync();  // no CTA leaves while another may read its tile
+    } else {
+        __syncthreads();
+    }
     if (warp == MMA_WARP) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, TMEM_COLS);
     }
 }
 
-// Once per device: the register split has to add up in the kernel as compiled, and
-// its shared memory is opted into.
-template <Mode MODE>
-cudaError_t set_up_once() {
-    static std::mutex lock;
-    static std::atomic<bool> done[64];
-    const int dev = current_device_info().device;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    std::lock_guard<std::mutex> hold(lock);
+// Once per device: the register split has to add up in the kernels as compiled, their
+// shared memory is opted into, and how many clusters of 2, 4 and 8 CTAs the device holds
+// at once is asked (the GPCs' SM counts leave some idle).
+struct DeviceSetup {
+    std::mutex lock;
+    std::atomic<bool> ready{false};
+    int clusters[4] = {0, 0, 0, 0};
+};
+
+template <Mode MODE, bool SPLIT>
+cudaError_t opt_in() {
     cudaFuncAttributes at;
-    cudaError_t e = cudaFuncGetAttributes(&at, k_product<MODE>);
+    const cudaError_t e = cudaFuncGetAttributes(&at, k_product<MODE, SPLIT>);
     if (e != cudaSuccess) return e;
     if (at.numRegs != REGS) return cudaErrorInvalidConfiguration;
-    e = cudaFuncSetAttribute(k_product<MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem_bytes<MODE>());
-    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return cudaFuncSetAttribute(k_product<MODE, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)smem_bytes<MODE>());
+}
+
+void split_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int size, int clusters, size_t smem,
+                  cudaStream_t s) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)size, 1, 1};
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    *cfg = cudaLaunchConfig_t{};
+    cfg->gridDim = dim3((unsigned)(clusters * size));
+    cfg->blockDim = dim3(THREADS);
+    cfg->dynamicSmemBytes = smem;
+    cfg->stream = s;
+    cfg->attrs = attr;
+    cfg->numAttrs = 2;
+}
+
+template <Mode MODE>
+cudaError_t set_up(DeviceSetup* d) {
+    std::lock_guard<std::mutex> hold(d->lock);
+    if (d->ready.load(std::memory_order_acquire)) return cudaSuccess;
+    cudaError_t e = opt_in<MODE, false>();
+    if (e == cudaSuccess) e = opt_in<MODE, true>();
+    for (int i = 1; e == cudaSuccess && i < 4; ++i) {
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg;
+        split_config(&cfg, attr, 1 << i, 1, smem_bytes<MODE>(), nullptr);
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&d->clusters[i], k_product<MODE, true>, &cfg);
+    }
+    if (e == cudaSuccess) d->ready.store(true, std::memory_order_release);
     return e;
 }
 
 template <Mode MODE>
-cudaError_t launch_tiles(const Fp8ProductArgs& a, cudaStream_t s) {
+cudaError_t launch_tiles(Fp8ProductArgs a, cudaStream_t s) {
     CUtensorMap ta, tb;
     bool ok;
-    int64_t tiles;
     if (MODE == kForward) {
         ok = make_tmap_2d(&ta, a.a, 1, a.M, a.K, BM, BK) &&
              make_tmap_2d(&tb, a.b, 1, (uint64_t)a.G * a.N, a.K, BN, BK);
@@ -640,17 +788,41 @@ cudaError_t launch_tiles(const Fp8ProductArgs& a, cudaStream_t s) {
              make_tmap_2d(&tb, a.b, 1, a.K, a.rows_t, BN, BK);
     }
     if (!ok) return cudaErrorInvalidValue;
-    if (MODE == kWeight)
-        tiles = (int64_t)a.G * (a.N / BM) * ((a.K + BN - 1) / BN);
-    else  // the groups' rows are known on the device only: at most this many
-        tiles = ((int64_t)a.M / BM + (a.G < a.M ? a.G : a.M)) *
-                (((MODE == kForward ? a.N : a.K) + BN - 1) / BN);
+    // the groups' rows are known on the device only: there at most this many tiles
+    const bool known = MODE == kWeight || a.offsets == nullptr;
+    const int groups = a.G < a.M ? a.G : a.M;
+    const int64_t tiles =
+        MODE == kWeight ? (int64_t)a.G * (a.N / BM) * ((a.K + BN - 1) / BN)
+                        : (known ? ((int64_t)a.M + BM - 1) / BM : (int64_t)a.M / BM + groups) *
+                              (((MODE == kForward ? a.N : a.K) + BN - 1) / BN);
     if (tiles >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
-    cudaError_t e = set_up_once<MODE>();
-    if (e != cudaSuccess) return e;
-    const int64_t sms = current_device_info().num_sms;
-    e = launch_pdl(k_product<MODE>, dim3((unsigned)(tiles < sms ? tiles : sms)),
-                   dim3(THREADS), smem_bytes<MODE>(), s, ta, tb, a);
+    static DeviceSetup setups[64];
+    const DevInfo& dev = current_device_info();
+    if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
+    DeviceSetup& d = setups[dev.device];
+    cudaError_t e;
+    if (!d.ready.load(std::memory_order_acquire) && (e = set_up<MODE>(&d)) != cudaSuccess) return e;
+
+    // Few tiles and a long sum: as many CTAs a tile as find room.  Measured, one CTA
+    // against the split: weight gradients of 1024 x 1024 (32 tiles, four CTAs each) over
+    // 2048 rows 15.2 against 16.6 us, 4096 rows 24.7 against 19.4, 16384 rows 80.8
+    // against 35.6; products of 1024 rows by 2048 columns (64 tiles, two each) with K =
+    // 4096 19.2 against 19.6 us, 6144 26.1 against 24.1, 8192 33.2 against 28.4.  (A
+    // launch of its own for the last wave's tiles, split so, gained 2% at 64 blocks
+    // and lost 4% at 32.)
+    const int64_t blocks = MODE == kWeight ? a.rows_t / BK / groups : (MODE == kForward ? a.K : a.N) / BK;
+    int lg = 0;
+    while (known && blocks >= (MODE == kWeight ? 32 : 48) && lg < 3 && tiles <= d.clusters[lg + 1]) ++lg;
+    if (lg > 0) {
+        a.split = 1 << lg;
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg;
+        split_config(&cfg, attr, a.split, (int)tiles, smem_bytes<MODE>(), s);
+        e = cudaLaunchKernelEx(&cfg, k_product<MODE, true>, ta, tb, a);
+    } else {
+        e = launch_pdl(k_product<MODE, false>, dim3((unsigned)(tiles < dev.num_sms ? tiles : dev.num_sms)),
+                       dim3(THREADS), smem_bytes<MODE>(), s, ta, tb, a);
+    }
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

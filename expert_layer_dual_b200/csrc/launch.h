@@ -243,6 +243,7 @@ struct Fp8ProductArgs {
     void* out;
     int out_type;            // MOE_OUT_*
     int accumulate;          // wgrad: add to out
+    int split;               // CTAs of a cluster that share a 128 x 256 tile
     int32_t* status;
     uint64_t timeout_ns;
 };

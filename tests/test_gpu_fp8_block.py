@@ -190,6 +190,45 @@ def test_weight_gradient_dense(shape, accumulate):
     check_rows(got, want, size, (rows + 127) // 128, torch.float32)
 
 
+# few tiles and long sums: rows, N, K, where a cluster of eight, four or two CTAs shares
+# the blocks of a tile; blocks that do not divide evenly and CTAs left without one.
+# (The cluster's sums round up to seven times more.)
+SPLIT_SUMS = [(4096, 512, 512), (4097, 128, 128), (4993, 256, 384), (5001, 1024, 1024), (4200, 1024, 2048),
+              (9345, 384, 640)]
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("shape", SPLIT_SUMS, ids=lambda s: "x".join(map(str, s)))
+def test_weight_gradient_of_long_sums(shape, accumulate):
+    rows, N, K = shape
+    got, want, size = weight_gradient(rows, N, K, 1, None, accumulate, rows)
+    check_rows(got, want, size, (rows + 127) // 128 + 7, torch.float32)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("sizes", [[9000, 0, 300], [4100, 4095], [1, 0, 16500]], ids=str)
+def test_weight_gradient_of_long_groups(sizes, accumulate):
+    """Groups without rows keep what was there, or become zeros."""
+    rows, off = make_groups(sizes, 2, 3)
+    got, want, size = weight_gradient(rows, 256, 384, len(sizes), off, accumulate, rows)
+    for g, n in enumerate(sizes):
+        check_rows(got[g], want[g], size[g], (n + 127) // 128 + 7, torch.float32)
+        if n == 0:
+            assert torch.equal(got[g], want[g].float())
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("op", ["forward", "input"])
+@pytest.mark.parametrize("shape", [(1024, 2048, 6144), (1001, 2176, 6272), (700, 2432, 8192)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_dense_long_sums(shape, op, dtype):
+    rows, cols, inner = shape
+    assert takes_wide_tiles(rows, cols)
+    N, K = (cols, inner) if op == "forward" else (inner, cols)
+    got, want, size, _ = product(op, rows, N, K, 1, None, TYPES[dtype], rows)
+    check_rows(got, want, size, inner // 128 + 1, TYPES[dtype])
+
+
 @pytest.mark.parametrize("accumulate", [False, True])
 @pytest.mark.parametrize("case", range(len(GROUPED)))
 def test_weight_gradient_grouped(case, accumulate):

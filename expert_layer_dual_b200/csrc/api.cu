@@ -949,7 +949,7 @@ moe_status moe_allreduce_rmsnorm_emulated(void* const* bufs, int32_t G, int32_t 
 
 namespace {
 struct BalanceLayout {
-    size_t psum, cnt, info, term, arrived, total;
+    size_t psum, cnt, info, total;
 };
 BalanceLayout balance_layout(int32_t T, int32_t E) {
     BalanceLayout L{};
@@ -964,8 +964,6 @@ BalanceLayout balance_layout(int32_t T, int32_t E) {
         L.psum = take(nb * E * 4);
         L.cnt = take(nb * E * 4);
         L.info = take(nb * 8);
-        L.term = take((size_t)E * 8);
-        L.arrived = take(4);
     }
     L.total = off;
     return L;
@@ -991,8 +989,7 @@ moe_status moe_balance_loss(const float* logits, const int32_t* ids, const uint8
     const moe_status r = check_ws(ws, ws_bytes, L.total);
     if (r != MOE_OK) return r;
     if (!device_ok()) return MOE_ERR_UNSUPPORTED;
-    const BalancePartials part{at<float>(ws, L.psum), at<int32_t>(ws, L.cnt), at<int32_t>(ws, L.info),
-                               at<double>(ws, L.term), at<int32_t>(ws, L.arrived)};
+    const BalancePartials part{at<float>(ws, L.psum), at<int32_t>(ws, L.cnt), at<int32_t>(ws, L.info)};
     const BalanceOut out{loss, counts, prob_mean, tokens, at<int32_t>(ws, 0), coef};
     return cuda_status(
         launch_balance_loss(logits, ids, mask, T, E, k, part, out, as_stream(stream)));

@@ -19,12 +19,13 @@
 // and a lane's values leave room for four blocks an SM, whose loads cover the
 // latency of memory.  Every logit is read once and every gradient written once, so
 // the bytes are the floor: 20 and 41 us for 131072 rows of 256 experts.  Measured
-// there: 29.7 us for the loss and 49.4 us for the gradient (4.5 and 5.4 TB/s).
+// there: 27.8 us for the loss and 47.4 us for the gradient (4.8 and 5.7 TB/s;
+// 49.7 us with the top-k part).
 // Other splits of a row took longer: a warp per row, with the accurate expf and
 // the top-k part by comparing every column with every id, 41 and 82 us, bound by
 // its instructions (210 and 496 a row); eight lanes with 32 values each 54 and 52
 // us, bound by the few warps its registers leave.  Few tokens are bound by the
-// launches: 4.1 and 3.5 us for 64.
+// launches: 4.0 and 3.5 us for 64.
 //
 // Sums are FP32 within a row and over a lane's rows, FP64 over the blocks; no
 // atomic on a float, so the results do not depend on scheduling.
@@ -39,7 +40,8 @@ constexpr int kRows = 32 / kLanes;       // rows of a warp
 constexpr int kGroup = 4 * kLanes;       // columns of a row read at once
 constexpr int kWarps = 8;                // warps per block
 constexpr int kOneWarps = 32;            // warps of the one-block kernel
-constexpr int kColBlock = 4;             // experts per block of k_balance_finish
+constexpr int kRowWarps = 16;            // warps of the two-pass form's blocks
+constexpr int kFinishBlocks = 8;         // of k_balance_finish: 32 experts each
 
 // NV: groups of 64 columns (E <= 64 NV); value 4i + c of lane l is column 64i + 4l + c.
 // VEC: E % 4 == 0, so the rows start on 16 bytes.
@@ -196,7 +198,6 @@ __global__ void __launch_bounds__(WARPS * 32)
         if (tid == 0) {
             part.info[2 * blockIdx.x] = s_tokens;
             part.info[2 * blockIdx.x + 1] = s_bad;
-            if (blockIdx.x == 0) *part.arrived = 0;
         }
         return;
     }
@@ -226,38 +227,37 @@ __global__ void __launch_bounds__(WARPS * 32)
     }
 }
 
-// Loss, second pass: a block sums the partials of kColBlock experts over the
-// first pass's blocks (in FP64, a fixed order; every load of a thread in flight
-// together) and leaves each expert's share of the loss; the last block to arrive
-// adds the E shares in order.
-__global__ void __launch_bounds__(256)
+// Loss, second pass: a cluster of eight blocks, 32 experts each.  Warp w takes the
+// partials of the first pass's blocks w, w + 32, .. (a row of 32 experts per load,
+// all of them in flight together); the sums over the warps are in FP64 and in a fixed
+// order, as is the sum of the eight blocks' shares of the loss in the first block's
+// shared memory.  (With 64 blocks of four experts, the last of which added the shares
+// through global memory, the loss took 11.0 us for 16384 tokens, so 8.4.)
+__global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(1024)
     k_balance_finish(int E, int k, int nblocks, BalancePartials part, BalanceOut out) {
-    constexpr int SLICES = 256 / kColBlock, PER = (kBalanceMaxBlocks + SLICES - 1) / SLICES;
-    __shared__ double s_sum[SLICES][kColBlock];
-    __shared__ int s_cnt[SLICES][kColBlock];
-    __shared__ int s_tokens[8], s_bad[8], s_last;
-    __shared__ double s_term[8];
+    constexpr int PER = (kBalanceMaxBlocks + 31) / 32;
+    __shared__ double s_sum[32][33];
+    __shared__ int s_cnt[32][33];
+    __shared__ int s_tokens[32], s_bad[32];
+    __shared__ double s_term[32], s_share[kFinishBlocks];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     pdl_wait();
-    const int e = blockIdx.x * kColBlock + tid % kColBlock, slice = tid / kColBlock;
+    const int e = blockIdx.x * 32 + lane;
     float p[PER];
     int c[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int b = slice + i * SLICES;
+        const int b = warp + i * 32;
         const bool in = e < E && b < nblocks;
         p[i] = in ? part.psum[(int64_t)b * E + e] : 0.0f;
         c[i] = in ? part.cnt[(int64_t)b * E + e] : 0;
     }
+    static_assert(kBalanceMaxBlocks <= 1024, "a thread per block of the first pass");
     int tokens = 0, bad = 0;
-#pragma unroll
-    for (int i = 0; i < (kBalanceMaxBlocks + 255) / 256; ++i) {
-        const int b = tid + 256 * i;
-        if (b < nblocks) {
-            tokens += part.info[2 * b];
-            bad |= part.info[2 * b + 1];
-        }
+    if (tid < nblocks) {
+        tokens = part.info[2 * tid];
+        bad = part.info[2 * tid + 1];
     }
     double sum = 0.0;
     int cnt = 0;
@@ -266,55 +266,47 @@ __global__ void __launch_bounds__(256)
         sum += p[i];
         cnt += c[i];
     }
-    // slices of the same expert within the warp (lanes kColBlock apart), then over the warps
-#pragma unroll
-    for (int o = kColBlock; o < 32; o <<= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
-    }
+    s_sum[warp][lane] = sum;
+    s_cnt[warp][lane] = cnt;
     tokens = __reduce_add_sync(0xffffffffu, tokens);
     bad = __reduce_or_sync(0xffffffffu, bad);
-    if (lane < kColBlock) {
-        s_sum[warp][lane] = sum;
-        s_cnt[warp][lane] = cnt;
-    }
     if (lane == 0) {
         s_tokens[warp] = tokens;
         s_bad[warp] = bad;
     }
     __syncthreads();
-    int n = 0, any = 0;
-    for (int w = 0; w < 8; ++w) {
-        n += s_tokens[w];
-        any |= s_bad[w];
-    }
-    if (tid < kColBlock && e < E) {
-        double s = 0.0;
-        int m = 0;
-        for (int w = 0; w < 8; ++w) {
-            s += s_sum[w][tid];
-            m += s_cnt[w][tid];
-        }
-        const double mean = n > 0 ? s / n : 0.0;
-        out.prob_mean[e] = (float)mean;
-        out.counts[e] = m;
-        part.term[e] = balance_fraction(m, E, (double)k * n) * mean;
-        __threadfence();
-    }
-    __syncthreads();
-    if (tid == 0) s_last = atomicAdd(part.arrived, 1) == (int)gridDim.x - 1;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    double term = tid < E ? __ldcg(part.term + tid) : 0.0;
+    // warp w: expert 32 blockIdx.x + w
+    const int n = __reduce_add_sync(0xffffffffu, s_tokens[lane]);
+    const int any = __reduce_or_sync(0xffffffffu, s_bad[lane]);
+    double s = s_sum[lane][warp];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
-    if (lane == 0) s_term[warp] = term;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int m = __reduce_add_sync(0xffffffffu, s_cnt[lane][warp]);
+    if (lane == 0) {
+        const int mine = blockIdx.x * 32 + warp;
+        const double mean = n > 0 ? s / n : 0.0;
+        if (mine < E) {
+            out.prob_mean[mine] = (float)mean;
+            out.counts[mine] = m;
+        }
+        s_term[warp] = mine < E ? balance_fraction(m, E, (double)k * n) * mean : 0.0;
+    }
     __syncthreads();
-    if (tid == 0) {
-        double s = 0.0;
-        for (int w = 0; w < 8; ++w) s += s_term[w];
-        *out.loss = (float)(out.coef * s);
+    if (warp == 0) {
+        double term = s_term[lane];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
+        if (lane == 0)
+            asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(smem_in_rank(&s_share[blockIdx.x], 0)), "d"(term)
+                         : "memory");
+    }
+    __syncwarp();
+    cluster_sync();
+    if (blockIdx.x == 0 && tid == 0) {
+        double total = 0.0;
+#pragma unroll
+        for (int b = 0; b < kFinishBlocks; ++b) total += s_share[b];
+        *out.loss = (float)(out.coef * total);
         *out.tokens = n;
         *out.status = any ? MOE_ERR_DEVICE_BAD_INDEX : MOE_OK;
     }
@@ -327,8 +319,10 @@ __global__ void __launch_bounds__(256)
 // repeat within a row are added up first, so their order does not matter.
 // Masked tokens get zeros and their logits are not read.
 // ---------------------------------------------------------------------------
+constexpr int backward_blocks(int nv) { return nv >= 3 ? 4 : nv == 2 ? 5 : 6; }  // per SM, by registers
+
 template <int NV, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, backward_blocks(NV))
     k_route_backward(const __grid_constant__ RouteBackwardArgs a) {
     constexpr int N = 4 * NV;
     __shared__ float s_row[kWarps][kRows][kGroup * NV];
@@ -422,12 +416,13 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
 }
 
-// The instance for E experts: groups of 64 columns, rounded up to 1, 2 or 4.
+// The instance for E experts: 1 to 4 groups of 64 columns.
 template <typename F>
 cudaError_t by_width(int E, F f) {
     const bool vec = E % 4 == 0;
     if (E <= kGroup) return vec ? f.template operator()<1, true>() : f.template operator()<1, false>();
     if (E <= 2 * kGroup) return vec ? f.template operator()<2, true>() : f.template operator()<2, false>();
+    if (E <= 3 * kGroup) return vec ? f.template operator()<3, true>() : f.template operator()<3, false>();
     return vec ? f.template operator()<4, true>() : f.template operator()<4, false>();
 }
 
@@ -444,7 +439,7 @@ struct LaunchRows {
         if (blocks == 1)
             return launch_pdl(k_balance_rows<NV, VEC, true, kOneWarps>, dim3(1), dim3(kOneWarps * 32), 0, s,
                               logits, ids, mask, T, E, k, part, out);
-        return launch_pdl(k_balance_rows<NV, VEC, false, kWarps>, dim3(blocks), dim3(kWarps * 32), 0, s,
+        return launch_pdl(k_balance_rows<NV, VEC, false, kRowWarps>, dim3(blocks), dim3(kRowWarps * 32), 0, s,
                           logits, ids, mask, T, E, k, part, out);
     }
 };
@@ -455,8 +450,11 @@ struct LaunchBackward {
     template <int NV, bool VEC>
     cudaError_t operator()() const {
         const int64_t want = ((int64_t)a.T + kWarps * kRows - 1) / (kWarps * kRows);
-        const int64_t most = (int64_t)current_device_info().num_sms * 6;
-        return launch_pdl(k_route_backward<NV, VEC>, dim3((unsigned)(want < most ? want : most)),
+        // as many blocks as are resident together, with turns of one length: 16384 tokens
+        // of 256 experts 10.2 us, 131072 49.7 us; with six per SM 10.9 and 55.7 us
+        const int64_t most = (int64_t)current_device_info().num_sms * backward_blocks(NV);
+        const int64_t turns = (want + most - 1) / most;
+        return launch_pdl(k_route_backward<NV, VEC>, dim3((unsigned)((want + turns - 1) / turns)),
                           dim3(kWarps * 32), 0, s, a);
     }
 };
@@ -465,11 +463,10 @@ struct LaunchBackward {
 
 int balance_blocks(int T) {
     if (T <= kBalanceOneBlock) return 1;
-    // a block per 64 tokens (the second pass reads a row of partials per block: with
-    // one per 16 16384 tokens took 11.2 us, so 8.7), but one per SM as soon as
-    // each has a turn's tokens
-    const int64_t few = ((int64_t)T + kWarps * kRows - 1) / (kWarps * kRows), many = ((int64_t)T + 63) / 64;
-    const int64_t want = few < 148 ? few : many < 148 ? 148 : many;
+    // 16 warps a block, two blocks an SM: with blocks of 8 (a block per 64 tokens, at most
+    // four an SM) 16384 tokens took 13.0 us and 2048 7.4, of 32 10.1 and 6.8, so 11.0
+    // and 6.3, the second pass at that time included
+    const int64_t want = ((int64_t)T + kRowWarps * kRows - 1) / (kRowWarps * kRows);
     return want < kBalanceMaxBlocks ? (int)want : kBalanceMaxBlocks;
 }
 
@@ -479,8 +476,7 @@ cudaError_t launch_balance_loss(const float* logits, const int32_t* ids, const u
     const int nb = balance_blocks(T);
     cudaError_t e = by_width(E, LaunchRows{logits, ids, mask, T, E, k, nb, part, out, s});
     if (e != cudaSuccess || nb == 1) return e != cudaSuccess ? e : cudaGetLastError();
-    e = launch_pdl(k_balance_finish, dim3((E + kColBlock - 1) / kColBlock), dim3(256), 0, s, E, k, nb,
-                   part, out);
+    e = launch_pdl(k_balance_finish, dim3(kFinishBlocks), dim3(1024), 0, s, E, k, nb, part, out);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

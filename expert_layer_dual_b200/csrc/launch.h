@@ -272,13 +272,11 @@ cudaError_t launch_quant_tokens(const uint16_t* x, const int32_t* offsets, int G
 
 // ---- balance.cu (load-balance loss, per-expert counts, gradient of the router logits)
 constexpr int kBalanceOneBlock = 128;   // up to this many tokens one block does it all
-constexpr int kBalanceMaxBlocks = 592;  // blocks of the first pass (four per SM)
+constexpr int kBalanceMaxBlocks = 296;  // blocks of the first pass (two per SM)
 struct BalancePartials {                // workspace of the two-pass form
     float* psum;       // [blocks][E]
     int32_t* cnt;      // [blocks][E]
     int32_t* info;     // [blocks][2]: tokens that count, an id out of range seen
-    double* term;      // [E]
-    int32_t* arrived;
 };
 struct BalanceOut {
     float* loss;

@@ -78,7 +78,8 @@ CASES = [
     dict(T=1, E=2, k=1), dict(T=1, E=256, k=8), dict(T=2, E=1, k=1), dict(T=7, E=8, k=8),
     dict(T=64, E=256, k=8), dict(T=100, E=60, k=4), dict(T=513, E=255, k=3), dict(T=511, E=33, k=5),
     dict(T=512, E=128, k=8), dict(T=2000, E=256, k=8), dict(T=3001, E=4, k=2), dict(T=5000, E=129, k=7),
-    dict(T=20011, E=64, k=6),
+    dict(T=20011, E=64, k=6), dict(T=4100, E=160, k=6), dict(T=9473, E=192, k=8), dict(T=9600, E=193, k=8),
+    dict(T=129, E=130, k=2),
 ]
 
 

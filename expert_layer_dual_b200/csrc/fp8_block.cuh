@@ -127,9 +127,11 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint64
     }
 }
 
-// Warp-collective: one outcome for the warp.
+// Warp-collective: one outcome for the warp.  The first try stands apart from the
+// bounded loop: most waits end with it.
 __device__ __forceinline__ bool warp_wait_phase(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
                                                 uint32_t abort_flag) {
+    if (__all_sync(0xffffffffu, try_phase(bar, parity))) return true;
     return __all_sync(0xffffffffu, wait_phase(bar, parity, timeout_ns, abort_flag));
 }
 

@@ -594,9 +594,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int row = quad * 32 + lane;
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * EPI_COLS;
         constexpr bool CS = MODE == kWeight;
-        Ring<STAGES> st;
+        uint32_t done = 0;  // blocks so far: their stages and partials follow from it
         Ring<SC_BUFS> ch;
-        uint32_t pb = 0;
         bool ok = true;
         for (int i = work.first; ok && i < work.total; i += work.step) {
             const int blocks = work.tile(a, sm.tt, i).blocks;
@@ -627,12 +626,12 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                         for (int g = 0; g < 4; ++g) c[g] = lds2(cs + 32 * g);
                     }
-                    if (!warp_wait_phase(sm.done(st.slot), st.round, a.timeout_ns, sm.abort_flag())) {
+                    if (!warp_wait_phase(sm.done(done % STAGES), done / STAGES & 1u, a.timeout_ns, sm.abort_flag())) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t p = taddr + pb * BN;
+                    const uint32_t pb = done % NPART, p = taddr + pb * BN;
                     auto release = [&] {  // the partial is in registers
                         tc_fence_before_sync();
                         __syncwarp();
@@ -674,8 +673,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             promote<32>(r, ff, acc + 16 * q);
                         }
                     }
-                    st.next();
-                    pb ^= 1u;
+                    ++done;
                 }
                 __syncwarp();
                 if (ok && elect_one()) arrive(sm.sempty(ch.slot));

@@ -280,7 +280,7 @@ __device__ __forceinline__ float block_scale(float amax) {
 // codes take their signs from the values; NaN has the code 0x7F whatever its sign.
 // (Bracketing the quotient between two roundings and dividing where they differ
 // was slower: bf16 values over a bf16 maximum meet exact ties in a group out of
-// seven.  8192 x 6144 values: 38 us so, 41 with divisions, 30.6 with the
+// seven.  8192 x 6144 values: 38 us so, 41 with divisions, 30.0 with the
 // correction.)
 struct GroupQuotient {
     float s, r;  // r = 0: divide

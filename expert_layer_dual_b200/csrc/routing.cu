@@ -604,29 +604,30 @@ __device__ __forceinline__ void quant_row(const uint16_t* __restrict__ src, int 
     }
 }
 
-// Rows as they are: a warp per 1024 columns of a row, its four 16-byte loads per
-// lane in flight together (a warp per row left 64 rows on eight SMs: 18 us at
-// 6144 columns); the codes by GroupQuotient, the same codes as quant_row's.
-__global__ void __launch_bounds__(256)
+// Rows as they are: a warp per 256 LOADS columns of a row, its 16-byte loads (LOADS per
+// lane) in flight together; the codes by GroupQuotient, the same codes as quant_row's.
+// (A warp per row left 64 rows on eight SMs: 18 us at 6144 columns.)
+template <int LOADS>
+__global__ void __launch_bounds__(256, 6)
     k_quant_act(const uint16_t* __restrict__ x, int64_t rows, int cols, uint8_t* __restrict__ q,
                 float* __restrict__ scale) {
     pdl_trigger();
     pdl_wait();
     const int64_t wid = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
-    const int nch = scatter_chunks(cols);
+    const int nch = (cols + 256 * LOADS - 1) / (256 * LOADS);
     const int64_t r = wid / nch;
     if (r >= rows) return;
     const int lane = threadIdx.x & 31;
-    const int c0 = (int)(wid - r * nch) * kScatterCols + lane * 8;
+    const int c0 = (int)(wid - r * nch) * (256 * LOADS) + lane * 8;
     const uint16_t* src = x + r * cols + c0;
-    uint4 u[4];
+    uint4 u[LOADS];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < LOADS; ++i) {
         u[i] = make_uint4(0, 0, 0, 0);
         if (c0 + i * 256 < cols) u[i] = __ldg(reinterpret_cast<const uint4*>(src + i * 256));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < LOADS; ++i) {
         uint32_t m = bf16x2_absmax4(u[i].x, u[i].y, u[i].z, u[i].w);
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) m = bf16x2_max(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -736,9 +737,16 @@ cudaError_t launch_quant_act_fp8_scatter(const uint16_t* x, const int32_t* inv, 
 cudaError_t launch_quant_act_fp8(const uint16_t* x, int64_t rows, int cols, uint8_t* q,
                                  float* scale, cudaStream_t s) {
     if (rows == 0) return cudaSuccess;
-    const int64_t warps = rows * ((cols + kScatterCols - 1) / kScatterCols);
-    const cudaError_t e = launch_pdl(k_quant_act, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, x,
-                                     rows, cols, q, scale);
+    // Long chunks for many rows, short ones where warps are few.  Measured with 1, 2 and 4
+    // loads: 1 x 2048 1.3, 1.6, 2.2 us; 64 x 6144 1.6, 1.9, 2.5; 3001 x 1408 (half a wave
+    // of warps with four loads) 4.4, 4.1, 4.8; 8192 x 1408 (one and a half) 11.0, 9.9,
+    // 10.3; 4096 x 4096 (two) 14.2, 12.9, 12.1; 8192 x 6144 39.4, 34.2, 30.0.
+    const int64_t wave = (int64_t)current_device_info().num_sms * 48, chunks = rows * cols / 1024;
+    const int loads = chunks >= 2 * wave ? 4 : chunks >= wave / 2 ? 2 : 1;
+    const int64_t warps = rows * ((cols + 256 * loads - 1) / (256 * loads));
+    const auto kernel = loads == 4 ? k_quant_act<4> : loads == 2 ? k_quant_act<2> : k_quant_act<1>;
+    const cudaError_t e = launch_pdl(kernel, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, x, rows, cols, q,
+                                     scale);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

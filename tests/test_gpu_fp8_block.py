@@ -471,6 +471,22 @@ def test_scale_of_every_bf16_maximum():
     assert torch.equal(s.cpu(), ws) and torch.equal(q.cpu(), wq)
 
 
+@pytest.mark.parametrize("shape", [(5, 2176), (2900, 1408), (1200, 3328), (10700, 1408), (4500, 3328)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_row_quantiser_exact(shape):
+    """One, two and four loads a warp, with rows that end inside a warp's columns, and
+    nothing written behind the rows."""
+    rows, cols = shape
+    x = randn(shape, rows)
+    x[:, 128:256] = 0
+    q = torch.full((rows + 1, cols), 0x55, dtype=torch.uint8, device=DEV)
+    s = torch.full((rows + 1, cols // 128), -1.0, device=DEV)
+    M.quantize_act_fp8(x.to(DEV), q[:rows], s[:rows])
+    wq, ws = ref.quantise_rows(x)
+    assert torch.equal(q[:rows].cpu(), wq) and torch.equal(s[:rows].cpu(), ws)
+    assert bool((q[rows] == 0x55).all()) and bool((s[rows] == -1.0).all())
+
+
 def test_codes_of_values_that_are_not_finite():
     """NaN and infinities in a group: the codes and scales are those of the quantiser
     of permuted rows (here in the rows' own order), which divides, and the same

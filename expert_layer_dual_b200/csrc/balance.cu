@@ -19,13 +19,13 @@
 // and a lane's values leave room for four blocks an SM, whose loads cover the
 // latency of memory.  Every logit is read once and every gradient written once, so
 // the bytes are the floor: 20 and 41 us for 131072 rows of 256 experts.  Measured
-// there: 27.8 us for the loss and 47.4 us for the gradient (4.8 and 5.7 TB/s;
+// there: 27.6 us for the loss and 47.4 us for the gradient (4.8 and 5.7 TB/s;
 // 49.7 us with the top-k part).
 // Other splits of a row took longer: a warp per row, with the accurate expf and
 // the top-k part by comparing every column with every id, 41 and 82 us, bound by
 // its instructions (210 and 496 a row); eight lanes with 32 values each 54 and 52
 // us, bound by the few warps its registers leave.  Few tokens are bound by the
-// launches: 4.0 and 3.5 us for 64.
+// launches: 3.7 and 3.3 us for 64.
 //
 // Sums are FP32 within a row and over a lane's rows, FP64 over the blocks; no
 // atomic on a float, so the results do not depend on scheduling.
@@ -45,8 +45,6 @@ constexpr int kFinishBlocks = 8;         // of k_balance_finish: 32 experts each
 
 // NV: groups of 64 columns (E <= 64 NV); value 4i + c of lane l is column 64i + 4l + c.
 // VEC: E % 4 == 0, so the rows start on 16 bytes.
-__device__ __forceinline__ int col_of(int v, int l) { return (v >> 2) * kGroup + l * 4 + (v & 3); }
-
 template <int NV, bool VEC>
 __device__ __forceinline__ void load_row(const float* row, int E, int l, float* v) {
 #pragma unroll
@@ -117,10 +115,6 @@ __device__ __forceinline__ float exp_row(float* v) {
     }
     s = row_sum(s);
     return s > 0.0f ? 1.0f / s : (s == 0.0f ? 0.0f : s);  // NaN stays NaN
-}
-
-__device__ __forceinline__ double balance_fraction(int count, int E, double kn) {
-    return kn > 0.0 ? (double)count * E / kn : 0.0;
 }
 
 // ---------------------------------------------------------------------------
@@ -203,15 +197,16 @@ __global__ void __launch_bounds__(WARPS * 32)
     }
     const int n = s_tokens;
     double term = 0.0;
+    const double inv = n > 0 ? 1.0 / ((double)k * n) : 0.0;
     if (tid < 256) {
         if (tid < E) {
             float s = 0.0f;
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) s += s_psum[w][tid];
-            const double mean = n > 0 ? (double)s / n : 0.0;
+            const double mean = s * inv * k;
             out.prob_mean[tid] = (float)mean;
             out.counts[tid] = s_cnt[tid];
-            term = balance_fraction(s_cnt[tid], E, (double)k * n) * mean;
+            term = (double)s_cnt[tid] * E * inv * mean;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
@@ -232,7 +227,7 @@ __global__ void __launch_bounds__(WARPS * 32)
 // all of them in flight together); the sums over the warps are in FP64 and in a fixed
 // order, as is the sum of the eight blocks' shares of the loss in the first block's
 // shared memory.  (With 64 blocks of four experts, the last of which added the shares
-// through global memory, the loss took 11.0 us for 16384 tokens, so 8.4.)
+// through global memory, the loss took 11.0 us for 16384 tokens, so 8.2.)
 __global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(1024)
     k_balance_finish(int E, int k, int nblocks, BalancePartials part, BalanceOut out) {
     constexpr int PER = (kBalanceMaxBlocks + 31) / 32;
@@ -284,12 +279,12 @@ __global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(1024)
     const int m = __reduce_add_sync(0xffffffffu, s_cnt[lane][warp]);
     if (lane == 0) {
         const int mine = blockIdx.x * 32 + warp;
-        const double mean = n > 0 ? s / n : 0.0;
+        const double inv = n > 0 ? 1.0 / ((double)k * n) : 0.0, mean = s * inv * k;
         if (mine < E) {
             out.prob_mean[mine] = (float)mean;
             out.counts[mine] = m;
         }
-        s_term[warp] = mine < E ? balance_fraction(m, E, (double)k * n) * mean : 0.0;
+        s_term[warp] = mine < E ? (double)m * E * inv * mean : 0.0;
     }
     __syncthreads();
     if (warp == 0) {
@@ -325,7 +320,7 @@ template <int NV, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32, backward_blocks(NV))
     k_route_backward(const __grid_constant__ RouteBackwardArgs a) {
     constexpr int N = 4 * NV;
-    __shared__ float s_row[kWarps][kRows][kGroup * NV];
+    __shared__ __align__(16) float s_row[kWarps][kRows][kGroup * NV], s_f1[kGroup * NV];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int l = lane % kLanes, r = lane / kLanes;
     float* const srow = s_row[warp][r];
@@ -340,13 +335,21 @@ __global__ void __launch_bounds__(kWarps * 32, backward_blocks(NV))
     for (int i = 0; i < N; ++i) f1[i] = 0.0f;
     if (balance) {
         const int n = *a.tokens;
-        const double kn = (double)k * n;
-        cb = n > 0 ? (float)((double)*a.dloss * a.coef / n) : 0.0f;
-        const double inv = n > 0 ? 1.0 / kn : 0.0;
+        cb = n > 0 ? *a.dloss * a.coef / (float)n : 0.0f;
+        // a quotient per thread, then each lane's columns (in FP64 and sixteen a thread, 4096
+        // tokens took 5.4 us, so 4.7)
+        if (tid < kGroup * NV) {
+            const int64_t kn = (int64_t)k * n;
+            s_f1[tid] = tid < E && n > 0 ? (float)((int64_t)a.counts[tid] * E - kn) / (float)kn : 0.0f;
+        }
+        __syncthreads();
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int c = col_of(i, l);
-            if (c < E) f1[i] = (float)(((double)a.counts[c] * E - kn) * inv);
+        for (int i = 0; i < NV; ++i) {
+            const float4 f = *reinterpret_cast<const float4*>(s_f1 + i * kGroup + l * 4);
+            f1[4 * i] = f.x;
+            f1[4 * i + 1] = f.y;
+            f1[4 * i + 2] = f.z;
+            f1[4 * i + 3] = f.w;
         }
     }
     const int64_t step = (int64_t)gridDim.x * kWarps * kRows;
@@ -451,7 +454,7 @@ struct LaunchBackward {
     cudaError_t operator()() const {
         const int64_t want = ((int64_t)a.T + kWarps * kRows - 1) / (kWarps * kRows);
         // as many blocks as are resident together, with turns of one length: 16384 tokens
-        // of 256 experts 10.2 us, 131072 49.7 us; with six per SM 10.9 and 55.7 us
+        // of 256 experts 10.1 us, 131072 49.8 us; with six per SM 10.9 and 55.7 us
         const int64_t most = (int64_t)current_device_info().num_sms * backward_blocks(NV);
         const int64_t turns = (want + most - 1) / most;
         return launch_pdl(k_route_backward<NV, VEC>, dim3((unsigned)((want + turns - 1) / turns)),

@@ -606,6 +606,8 @@ __device__ __forceinline__ void quant_row(const uint16_t* __restrict__ src, int 
 
 // Rows as they are: a warp per 256 LOADS columns of a row, its 16-byte loads (LOADS per
 // lane) in flight together; the codes by GroupQuotient, the same codes as quant_row's.
+// The bytes bound it (2 read and 1 written per value), its instructions close behind:
+// with a chain of exchanges and a scale per load 8192 x 6144 took 30.0 us, so 26.9.
 // (A warp per row left 64 rows on eight SMs: 18 us at 6144 columns.)
 template <int LOADS>
 __global__ void __launch_bounds__(256, 6)
@@ -626,22 +628,37 @@ __global__ void __launch_bounds__(256, 6)
         u[i] = make_uint4(0, 0, 0, 0);
         if (c0 + i * 256 < cols) u[i] = __ldg(reinterpret_cast<const uint4*>(src + i * 256));
     }
+    // the maxima of two groups (load i and i + 1) in a word through the exchanges
+    uint32_t top[(LOADS + 1) / 2];
+#pragma unroll
+    for (int i = 0; i < LOADS; i += 2) {
+        const int k = i + 1 < LOADS ? i + 1 : i;
+        const uint32_t a = bf16x2_absmax4(u[i].x, u[i].y, u[i].z, u[i].w);
+        const uint32_t b = k == i ? a : bf16x2_absmax4(u[k].x, u[k].y, u[k].z, u[k].w);
+        top[i / 2] = bf16x2_max(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < (LOADS + 1) / 2; ++i)
+            top[i] = bf16x2_max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+    // each of a half warp's lanes has one load's group, LOADS of them in turn
+    const int mine = lane & (LOADS - 1);
+    const uint32_t pair = LOADS == 4 && (mine & 2) ? top[(LOADS - 1) / 2] : top[0];
+    const GroupQuotient own(block_scale(__uint_as_float((mine & 1) ? pair & 0xFFFF0000u : pair << 16)));
+    {
+        const int c = c0 + mine * 256;
+        if ((lane & 15) < LOADS && c < cols) scale[r * (cols / 128) + c / 128] = own.s;
+    }
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
-        uint32_t m = bf16x2_absmax4(u[i].x, u[i].y, u[i].z, u[i].w);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = bf16x2_max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float amax = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
-        const GroupQuotient g(block_scale(amax));
+        const GroupQuotient g(__shfl_sync(0xffffffffu, own.s, (lane & 16) | i),
+                              __shfl_sync(0xffffffffu, own.r, (lane & 16) | i));
         const int c = c0 + i * 256;
-        if (c < cols) {
+        if (c < cols)
             *reinterpret_cast<uint2*>(q + r * cols + c) =
-                make_uint2(g.codes4(bf16x2_widen(u[i].x), bf16x2_widen(u[i].y),
-                                    __byte_perm(u[i].x, u[i].y, 0x7531)),
-                           g.codes4(bf16x2_widen(u[i].z), bf16x2_widen(u[i].w),
-                                    __byte_perm(u[i].z, u[i].w, 0x7531)));
-            if ((lane & 15) == 0) scale[r * (cols / 128) + c / 128] = g.s;
-        }
+                make_uint2(g.codes4(bf16x2_widen(u[i].x), bf16x2_widen(u[i].y)),
+                           g.codes4(bf16x2_widen(u[i].z), bf16x2_widen(u[i].w)));
     }
 }
 
@@ -738,11 +755,12 @@ cudaError_t launch_quant_act_fp8(const uint16_t* x, int64_t rows, int cols, uint
                                  float* scale, cudaStream_t s) {
     if (rows == 0) return cudaSuccess;
     // Long chunks for many rows, short ones where warps are few.  Measured with 1, 2 and 4
-    // loads: 1 x 2048 1.3, 1.6, 2.2 us; 64 x 6144 1.6, 1.9, 2.5; 3001 x 1408 (half a wave
-    // of warps with four loads) 4.4, 4.1, 4.8; 8192 x 1408 (one and a half) 11.0, 9.9,
-    // 10.3; 4096 x 4096 (two) 14.2, 12.9, 12.1; 8192 x 6144 39.4, 34.2, 30.0.
+    // loads: 1 x 2048 1.4, 1.5, 1.9 us; 64 x 6144 1.7, 1.7, 2.2; 512 x 4096 2.7, 3.0, 3.9;
+    // 3001 x 1408 (half a wave of warps with four loads) 4.5, 3.7, 4.3; 2048 x 4096 (a
+    // wave) 7.3, 5.9, 6.0; 4096 x 4096 (two) 14.4, 12.3, 10.8; 8192 x 6144 40.3, 32.5,
+    // 26.9 (5.6 TB/s).
     const int64_t wave = (int64_t)current_device_info().num_sms * 48, chunks = rows * cols / 1024;
-    const int loads = chunks >= 2 * wave ? 4 : chunks >= wave / 2 ? 2 : 1;
+    const int loads = chunks >= wave ? 4 : chunks >= wave / 2 ? 2 : 1;
     const int64_t warps = rows * ((cols + 256 * loads - 1) / (256 * loads));
     const auto kernel = loads == 4 ? k_quant_act<4> : loads == 2 ? k_quant_act<2> : k_quant_act<1>;
     const cudaError_t e = launch_pdl(kernel, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, x, rows, cols, q,

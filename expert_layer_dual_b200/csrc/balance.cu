@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(WARPS * 32)
                    const uint8_t* __restrict__ mask, int T, int E, int k, BalancePartials part,
                    BalanceOut out) {
     constexpr int N = 4 * NV;
-    __shared__ float s_psum[WARPS][kGroup * NV];
+    __shared__ __align__(16) float s_psum[WARPS][kGroup * NV];
     __shared__ int s_cnt[256], s_tokens, s_bad;
     __shared__ double s_term[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

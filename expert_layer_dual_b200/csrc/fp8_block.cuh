@@ -63,15 +63,51 @@ __device__ __forceinline__ void build_group_table(TileTable* tt, const int32_t* 
     __syncwarp();
 }
 
-// The group that owns tile `tile` of a table with one n-tile per row tile
-// (mstart[g] <= tile < mstart[g+1]); tile < mstart[G].
-__device__ __forceinline__ int group_of(const TileTable* tt, int G, int tile) {
-    int lo = 0, hi = G;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (tt->mstart[mid] <= tile) lo = mid; else hi = mid;
+// One warp: the first row, and the end of its group, of block `blk` of the groups' rows
+// in blocks of 128 (rows of the table above, without a table: a scan over the
+// lanes' groups in registers); false past the last block.
+__device__ __forceinline__ bool locate_block(const int32_t* __restrict__ offsets, int G, int M, int blk,
+                                             int* row0, int* end) {
+    const int lane = threadIdx.x & 31;
+    const int per = (G + 31) / 32;
+    const int g0 = min(G, lane * per), g1 = min(G, g0 + per);
+    auto offset = [&](int g) { return min(M, max(0, __ldg(offsets + g))); };
+    int top = 0;
+    for (int g = g0; g < g1; ++g) top = max(top, offset(g));
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, top, o);
+        if (lane >= o) top = max(top, v);
     }
-    return lo;
+    int before = __shfl_up_sync(0xffffffffu, top, 1);
+    if (lane == 0) before = 0;
+    int sum = 0;
+    for (int g = g0, at = before; g < g1; ++g) {
+        at = max(at, offset(g));
+        sum += (max(at, offset(g + 1)) - at + 127) / 128;
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, incl > blk);
+    if (past == 0) return false;
+    int r = 0, e = 0, left = blk - (incl - sum);  // of the first lane past it
+    for (int g = g0, at = before; g < g1; ++g) {
+        at = max(at, offset(g));
+        const int next = max(at, offset(g + 1)), n = (next - at + 127) / 128;
+        if (left >= 0 && left < n) {
+            r = at + left * 128;
+            e = next;
+        }
+        left -= n;
+    }
+    const int owner = __ffs(past) - 1;
+    *row0 = __shfl_sync(0xffffffffu, r, owner);
+    *end = __shfl_sync(0xffffffffu, e, owner);
+    return true;
 }
 
 // ---------------------------------------------------------------- device helpers

@@ -840,20 +840,27 @@ constexpr int QC = 64;
 __global__ void __launch_bounds__(256)
     k_quant_tokens(const uint16_t* __restrict__ x, const int32_t* __restrict__ offsets, int G, int M,
                    int cols, int64_t rows_t, uint8_t* __restrict__ q, float* __restrict__ scale) {
-    __shared__ TileTable tt;
-    __shared__ uint32_t red[8][QC / 2];
-    __shared__ float2 quot[QC];
+    __shared__ int2 s_rows;
+    __shared__ __align__(16) uint32_t red[8][QC / 2];  // read and written 16 bytes at a time
+    __shared__ __align__(16) float2 quot[QC];
     __shared__ uint32_t codes[QC][33];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     pdl_wait();
-    if (warp == 0) build_group_table(&tt, offsets, G, M, 128);
-    __syncthreads();
     const int blk = blockIdx.y;
-    if (blk >= tt.mstart[G]) return;
-    const int g = group_of(&tt, G, blk);
-    const int64_t row0 = tt.goff[g] + (int64_t)(blk - tt.mstart[g]) * 128;
-    const int rows = min((int64_t)128, tt.goff[g + 1] - row0);
+    int64_t row0 = (int64_t)blk * 128, end = M;  // one group: its rows in order
+    if (offsets != nullptr) {
+        if (warp == 0) {
+            int first = 0, last = -1;
+            if (!locate_block(offsets, G, M, blk, &first, &last)) last = -1;
+            if (lane == 0) s_rows = make_int2(first, last);
+        }
+        __syncthreads();
+        row0 = s_rows.x;
+        end = s_rows.y;
+        if (end < 0) return;
+    }
+    const int rows = (int)min((int64_t)128, end - row0);
     // a thread: four tokens of eight columns, a word holding two columns
     const int c0 = blockIdx.x * QC, c8 = (tid & 7) * 8, r4 = (tid >> 3) * 4;
     uint32_t w[4][4], m[4];

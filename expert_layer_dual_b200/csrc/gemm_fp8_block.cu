@@ -832,8 +832,10 @@ cudaError_t launch_tiles(Fp8ProductArgs a, cudaStream_t s) {
 // threads takes 128 tokens x 64 columns: 16-byte loads, the column maxima by
 // shuffles and shared memory, and the codes turned in shared memory so that
 // each column's 128 codes leave as one 128-byte run.  2 bytes are read and 1
-// written per value: 8192 x 6144 values take 32.3 us (4.7 TB/s; 47 us with an
-// IEEE division per value, which bound it).
+// written per value: 8192 x 6144 values take 31.5 us (4.8 TB/s; 47 us with an
+// IEEE division per value, which bound it), in 32 ragged groups 45.4.  Eight blocks an
+// SM, in 32 registers with spills, took 30.5 and 41.9 us there, but 5.6 for 5.0 us with
+// 3001 x 1408: not taken.
 // ---------------------------------------------------------------------------
 constexpr int QC = 64;
 
@@ -891,17 +893,22 @@ __global__ void __launch_bounds__(256)
         quot[tid] = make_float2(q8.s, q8.r);
     }
     __syncthreads();
+    if (warp * 16 < rows) {  // (without this rule the ragged groups above took 47.5 us)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        // the two columns of word j, four tokens each: the words' low and high halves
-        const uint32_t a = w[0][j], b = w[1][j], c = w[2][j], d = w[3][j];
-        const float4 t = *reinterpret_cast<const float4*>(&quot[c8 + 2 * j]);
-        codes[c8 + 2 * j][tid >> 3] = GroupQuotient(t.x, t.y).codes4(
-            f32x2_pack(__uint_as_float(a << 16), __uint_as_float(b << 16)),
-            f32x2_pack(__uint_as_float(c << 16), __uint_as_float(d << 16)));
-        codes[c8 + 2 * j + 1][tid >> 3] = GroupQuotient(t.z, t.w).codes4(
-            f32x2_pack(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u)),
-            f32x2_pack(__uint_as_float(c & 0xFFFF0000u), __uint_as_float(d & 0xFFFF0000u)));
+        for (int j = 0; j < 4; ++j) {
+            // the two columns of word j, four tokens each: the words' low and high halves
+            const uint32_t a = w[0][j], b = w[1][j], c = w[2][j], d = w[3][j];
+            const float4 t = *reinterpret_cast<const float4*>(&quot[c8 + 2 * j]);
+            codes[c8 + 2 * j][tid >> 3] = GroupQuotient(t.x, t.y).codes4(
+                f32x2_pack(__uint_as_float(a << 16), __uint_as_float(b << 16)),
+                f32x2_pack(__uint_as_float(c << 16), __uint_as_float(d << 16)));
+            codes[c8 + 2 * j + 1][tid >> 3] = GroupQuotient(t.z, t.w).codes4(
+                f32x2_pack(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u)),
+                f32x2_pack(__uint_as_float(c & 0xFFFF0000u), __uint_as_float(d & 0xFFFF0000u)));
+        }
+    } else {  // none of the warp's tokens
+#pragma unroll
+        for (int j = 0; j < 8; ++j) codes[c8 + j][tid >> 3] = 0;
     }
     __syncthreads();
 #pragma unroll

@@ -55,8 +55,9 @@ bool make_tmap_2d(CUtensorMap* map, const void* base, int elem_bytes, uint64_t r
                   uint64_t cols, uint32_t box_rows, uint32_t box_cols) {
     EncodeTiledFn fn = encode_tiled();
     if (fn == nullptr || base == nullptr || rows == 0 || cols == 0) return false;
-    const CUtensorMapDataType dt =
-        elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const CUtensorMapDataType dt = elem_bytes == 4   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : elem_bytes == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                     : CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const cuuint64_t dims[2] = {cols, rows};
     const cuuint64_t strides[1] = {cols * (cuuint64_t)elem_bytes};
     const cuuint32_t box[2] = {box_cols, box_rows};

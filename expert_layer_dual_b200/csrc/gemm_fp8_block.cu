@@ -20,7 +20,10 @@ namespace {
 enum Mode { kForward, kInput, kWeight };
 
 constexpr int BM = 128, BN = 256, BK = 128;    // a tile's rows and columns; one scale block of the sum
-constexpr int STAGES = 4, A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int MAX_STAGES = 4;                  // operands of as many blocks;
+template <Mode MODE>                           // kWeight: three, and the output on its way out
+constexpr int kStages = MODE == kWeight ? 3 : MAX_STAGES;
 constexpr int NPART = 2;                       // partial buffers of BN TMEM columns
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int EPI_WARPS = 16;                  // epilogue warps, EPI_COLS columns each
@@ -32,7 +35,11 @@ constexpr int THREADS = 32 * (SCALE_WARP + 1);
 // sixteen epilogue warps (64 accumulators each) rise to 112: 512 * 112 + 128 * 32
 // = 640 * 96 (checked against the compiled kernel before its first launch).
 constexpr int REGS = 96, REGS_EPI = 112, REGS_HELP = 32;
-constexpr int SC_KB = 4, SC_BUFS = 4;           // scales: chunks of 4 blocks, four chunks ahead
+constexpr int SC_KB = 4, MAX_SC_BUFS = 4;       // scales: chunks of 4 blocks,
+template <Mode MODE>
+constexpr int kScBufs = MODE == kWeight ? 2 : MAX_SC_BUFS;  // as many ahead
+constexpr int OUT_ATOM = 8 * 128;               // kWeight: 8 rows x 32 columns of the output,
+constexpr int OUT_WARP = 4 * OUT_ATOM;          // two pairs of them per epilogue warp
 
 // One chunk of scales, in floats: the CTA's 128 row scales of SC_KB blocks
 // ([row][block] for kForward and kInput, as they lie in memory; [block][row] for
@@ -41,28 +48,29 @@ template <Mode MODE>
 struct ScaleLayout {
     static constexpr int COLS = BM * SC_KB;  // where the column side's start
     static constexpr int CHUNK = COLS + SC_KB * (MODE == kWeight ? BN : 4);
-    static constexpr int FLOATS = SC_BUFS * CHUNK;
+    static constexpr int FLOATS = kScBufs<MODE> * CHUNK;
 };
 
 struct Bars {
-    uint64_t full[STAGES];      // two arming arrivals (A and B) + their bytes
-    uint64_t done[STAGES];      // MMA commit: the stage is free, the block's partial complete
+    uint64_t full[MAX_STAGES];  // two arming arrivals (A and B) + their bytes
+    uint64_t done[MAX_STAGES];  // MMA commit: the stage is free, the block's partial complete
     uint64_t pempty[NPART];     // partial read (one arrival per epilogue warp)
-    uint64_t sfull[SC_BUFS];    // scale chunk landed (32 asynchronous arrivals)
-    uint64_t sempty[SC_BUFS];   // scale chunk read (one arrival per epilogue warp)
+    uint64_t sfull[MAX_SC_BUFS];   // scale chunk landed (32 asynchronous arrivals)
+    uint64_t sempty[MAX_SC_BUFS];  // scale chunk read (one arrival per epilogue warp)
     uint32_t tmem_slot;
     int abort_flag;
 };
 
 template <Mode MODE>
 constexpr size_t smem_bytes() {
-    return 1024 + STAGES * STAGE_BYTES + ScaleLayout<MODE>::FLOATS * 4 + sizeof(Bars) +
+    return 1024 + kStages<MODE> * STAGE_BYTES + (MODE == kWeight ? EPI_WARPS * OUT_WARP : 0) +
+           ScaleLayout<MODE>::FLOATS * 4 + sizeof(Bars) +
            sizeof(TileTable) + 64;
 }
 
 // The block's shared memory, by shared addresses.
 struct Smem {
-    uint32_t stages, scales, bars;
+    uint32_t stages, out, scales, bars;
     TileTable* tt;
     __device__ __forceinline__ uint32_t full(int i) const { return bars + offsetof(Bars, full) + 8 * i; }
     __device__ __forceinline__ uint32_t done(int i) const { return bars + offsetof(Bars, done) + 8 * i; }
@@ -134,7 +142,7 @@ struct Work {
 };
 
 // ---------------------------------------------------------------- scales
-// The scale warp: keeps SC_BUFS chunks of SC_KB blocks' scales in flight ahead of
+// The scale warp: keeps kScBufs chunks of SC_KB blocks' scales in flight ahead of
 // the epilogue (asynchronous copies that arrive on the chunk's barrier by
 // themselves).  16-byte copies where the layout allows (four blocks of a row, or
 // four columns, side by side and aligned), else 4-byte ones.  Rows and columns
@@ -148,7 +156,7 @@ __device__ __forceinline__ void scale_role(const Fp8ProductArgs& a, const Smem& 
     const int per_row = MODE == kForward ? kbs : nb;
     const bool wide = MODE == kWeight ? aligned16(a.a_scale) && aligned16(a.b_scale)
                                       : aligned16(a.a_scale) && per_row % 4 == 0;
-    Ring<SC_BUFS> ring;
+    Ring<kScBufs<MODE>> ring;
     bool ok = true;
     for (int i = work.first; ok && i < work.total; i += work.step) {
         const PTile t = work.tile(a, sm.tt, i);
@@ -234,13 +242,12 @@ __device__ __forceinline__ void promote_scaled(const uint32_t* r, float f0, floa
     }
 }
 
-// Four chunks of W words in each of four neighbouring lanes, turned: lane j of the
+// Four chunks of eight words in each of four neighbouring lanes, turned: lane j of the
 // four ends with chunk j of all four lanes, in lane order.  The accumulators hold
 // a row per lane; turned, the four lanes store 128 consecutive bytes of one row
 // at a time.  (A store of 32 bytes from each of 32 rows kept the store unit four
 // times as long: the weight gradients of 32 small experts, 369 MB, took
 // 103 us, so 85.)
-template <int W>
 __device__ __forceinline__ void turn_chunks(uint32_t* v) {
     const int j = threadIdx.x & 3;
 #pragma unroll
@@ -250,8 +257,8 @@ __device__ __forceinline__ void turn_chunks(uint32_t* v) {
         for (int k = 0; k < 4; ++k) {
             if (k & step) continue;
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                uint32_t &lo = v[W * k + w], &hi = v[W * (k + step) + w];
+            for (int w = 0; w < 8; ++w) {
+                uint32_t &lo = v[8 * k + w], &hi = v[8 * (k + step) + w];
                 const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, step);
                 if (up) lo = got; else hi = got;
             }
@@ -271,42 +278,13 @@ __device__ __forceinline__ void store8(uint32_t* p, const uint32_t* v) {
     }
 }
 
-// Writes a warp's 32 rows x EPI_COLS columns: row0 is the output row of lane 0, `valid`
+// kForward, kInput: writes a warp's 32 rows x EPI_COLS columns: row0 is the output row of lane 0, `valid`
 // of the rows are stored, acc the lane's row.
-template <Mode MODE>
 __device__ __forceinline__ void store_tile(const Fp8ProductArgs& a, int64_t row0, int valid, int cols, int col,
                                            const uint64_t* acc) {
     static_assert(EPI_COLS == 64, "two halves of 32 words, or one of 32 pairs");
     const int lane = threadIdx.x & 31, first = lane & ~3, j = lane & 3;
-    if (MODE == kWeight) {
-        // rows l / 4 + 8 q, of each eight columns a pair: turned, eight columns of each 32
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t w[8];
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float lo, hi;
-                    f32x2_unpack(acc[8 * q + 4 * h + g], lo, hi);
-                    w[2 * g] = __float_as_uint(lo);
-                    w[2 * g + 1] = __float_as_uint(hi);
-                }
-                turn_chunks<2>(w);
-                float* dst = static_cast<float*>(a.out) + (row0 + 8 * q + (lane >> 2)) * cols + col + 32 * h + 8 * j;
-                if (a.accumulate) {
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float4 o = *reinterpret_cast<const float4*>(dst + 4 * i);
-                        w[4 * i] = __float_as_uint(__uint_as_float(w[4 * i]) + o.x);
-                        w[4 * i + 1] = __float_as_uint(__uint_as_float(w[4 * i + 1]) + o.y);
-                        w[4 * i + 2] = __float_as_uint(__uint_as_float(w[4 * i + 2]) + o.z);
-                        w[4 * i + 3] = __float_as_uint(__uint_as_float(w[4 * i + 3]) + o.w);
-                    }
-                }
-                store8(reinterpret_cast<uint32_t*>(dst), w);
-            }
-    } else if (a.out_type == MOE_OUT_F32) {
+    if (a.out_type == MOE_OUT_F32) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint32_t w[32];
@@ -317,7 +295,7 @@ __device__ __forceinline__ void store_tile(const Fp8ProductArgs& a, int64_t row0
                 w[2 * i] = __float_as_uint(lo);
                 w[2 * i + 1] = __float_as_uint(hi);
             }
-            turn_chunks<8>(w);
+            turn_chunks(w);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (first + i >= valid) break;
@@ -334,7 +312,7 @@ __device__ __forceinline__ void store_tile(const Fp8ProductArgs& a, int64_t row0
             f32x2_unpack(acc[i], lo, hi);
             w[i] = f16 ? pack_f16x2_sat(lo, hi) : pack_bf16x2(lo, hi);
         }
-        turn_chunks<8>(w);
+        turn_chunks(w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (first + i >= valid) break;
@@ -344,11 +322,68 @@ __device__ __forceinline__ void store_tile(const Fp8ProductArgs& a, int64_t row0
     }
 }
 
+template <int PENDING>  // bulk stores of this thread that may still read shared memory
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(PENDING) : "memory");
+}
+template <int PENDING>
+__device__ __forceinline__ void bulk_wait() {
+    asm volatile("cp.async.bulk.wait_group %0;" ::"n"(PENDING) : "memory");
+}
+
+// kWeight: sends a warp's 32 rows x EPI_COLS columns on their way through shared memory
+// (`buf`, two slots of eight rows), while the warp goes on to the next tile.  In
+// shared memory the rows of 32 columns lie as the tensor map's 128-byte swizzle has
+// them: 16-byte piece p of row r in place p ^ r.  A lane has row l / 4 and of each
+// eight columns a pair; odd rows take the groups of eight in another order, so that
+// the stores of half a warp fall on distinct banks.
+__device__ __forceinline__ void send_tile(const Fp8ProductArgs& a, const CUtensorMap* map, uint32_t buf,
+                                          int64_t row0, int col, uint64_t* acc) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
+    const bool odd = (r & 1) != 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        if (a.accumulate) {
+            const float* old = static_cast<const float*>(a.out) + (row0 + 8 * q + r) * a.K + col + 2 * j;
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+                const float2 o = *reinterpret_cast<const float2*>(old + 8 * g);
+                float lo, hi;
+                f32x2_unpack(acc[8 * q + g], lo, hi);
+                acc[8 * q + g] = f32x2_pack(lo + o.x, hi + o.y);
+            }
+        }
+        const uint32_t slot = buf + (q & 1) * 2 * OUT_ATOM;
+        if (lane == 0) bulk_wait_read<1>();  // what was sent from this slot last
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint64_t v = odd ? acc[8 * q + 4 * h + (g ^ 2)] : acc[8 * q + 4 * h + g];
+                const int piece = (2 * (odd ? g ^ 2 : g) + (j >> 1)) ^ r;
+                asm volatile("st.shared.b64 [%0], %1;" ::"r"(slot + h * OUT_ATOM + 128 * r + 16 * piece + 8 * (j & 1)),
+                             "l"(v)
+                             : "memory");
+            }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+                             "r"(col + 32 * h), "r"((int)(row0 + 8 * q)), "r"(slot + h * OUT_ATOM)
+                             : "memory");
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+        }
+    }
+}
+
 // A tile split over a cluster: every CTA leaves its sums in its shared memory (where
 // the operands were: every MMA that read them is complete), and adds its share of
 // the rows over the CTAs, in rank order.
 constexpr int LEFT_COLS = BN + 8;  // of a row: eight rows' pairs, or quarters, on distinct banks
-static_assert(BM * LEFT_COLS * 4 <= STAGES * STAGE_BYTES, "the tile fits where the operands were");
+static_assert(BM * LEFT_COLS * 4 <= 3 * STAGE_BYTES, "the tile fits where the operands were");
 
 template <Mode MODE>
 __device__ __forceinline__ void leave_tile(const Smem& sm, int quad, int part, int lane, const uint64_t* acc) {
@@ -460,13 +495,15 @@ __device__ __forceinline__ void add_tiles(const Fp8ProductArgs& a, const Smem& s
 template <Mode MODE, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
     k_product(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                   const __grid_constant__ Fp8ProductArgs a) {
+              const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ Fp8ProductArgs a) {
     extern __shared__ uint8_t smem_raw[];
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     using SL = ScaleLayout<MODE>;
+    constexpr int STAGES = kStages<MODE>;
     Smem sm;
     sm.stages = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    sm.scales = sm.stages + STAGES * STAGE_BYTES;
+    sm.out = sm.stages + STAGES * STAGE_BYTES;
+    sm.scales = sm.out + (MODE == kWeight ? EPI_WARPS * OUT_WARP : 0);
     sm.bars = sm.scales + 4 * SL::FLOATS;
     Bars* const b = reinterpret_cast<Bars*>(smem_raw + (sm.bars - smem_u32(smem_raw)));
     sm.tt = reinterpret_cast<TileTable*>(b + 1);
@@ -477,7 +514,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(&b->done[s], 1);
         }
         for (int i = 0; i < NPART; ++i) mbar_init(&b->pempty[i], EPI_WARPS);
-        for (int i = 0; i < SC_BUFS; ++i) {
+        for (int i = 0; i < kScBufs<MODE>; ++i) {
             mbar_init(&b->sfull[i], 32);
             mbar_init(&b->sempty[i], EPI_WARPS);
         }
@@ -595,7 +632,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) + part * EPI_COLS;
         constexpr bool CS = MODE == kWeight;
         uint32_t done = 0;  // blocks so far: their stages and partials follow from it
-        Ring<SC_BUFS> ch;
+        Ring<kScBufs<MODE>> ch;
         bool ok = true;
         for (int i = work.first; ok && i < work.total; i += work.step) {
             const int blocks = work.tile(a, sm.tt, i).blocks;
@@ -692,10 +729,14 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int col = t.col0 + part * EPI_COLS;
             if (col < cols && !(MODE == kWeight && a.accumulate && t.blocks == 0)) {
                 const int64_t row0 = MODE == kWeight ? (int64_t)t.g * a.N + t.row0 : t.row0;
-                store_tile<MODE>(a, row0 + quad * 32, t.nrows - quad * 32, cols, col, acc);
+                if constexpr (MODE == kWeight)
+                    send_tile(a, &tm_out, sm.out + warp * OUT_WARP, row0 + quad * 32, col, acc);
+                else
+                    store_tile(a, row0 + quad * 32, t.nrows - quad * 32, cols, col, acc);
             }
             __syncwarp();
         }
+        if (MODE == kWeight && !SPLIT && lane == 0) bulk_wait<0>();  // the output has left
         if constexpr (SPLIT) {
             __syncwarp();
             cluster_sync();  // every CTA's tile is in its shared memory
@@ -773,7 +814,7 @@ cudaError_t set_up(DeviceSetup* d) {
 
 template <Mode MODE>
 cudaError_t launch_tiles(Fp8ProductArgs a, cudaStream_t s) {
-    CUtensorMap ta, tb;
+    CUtensorMap ta, tb, tout;
     bool ok;
     if (MODE == kForward) {
         ok = make_tmap_2d(&ta, a.a, 1, a.M, a.K, BM, BK) &&
@@ -785,6 +826,10 @@ cudaError_t launch_tiles(Fp8ProductArgs a, cudaStream_t s) {
         ok = make_tmap_2d(&ta, a.a, 1, a.N, a.rows_t, BM, BK) &&
              make_tmap_2d(&tb, a.b, 1, a.K, a.rows_t, BN, BK);
     }
+    if (MODE == kWeight)
+        ok = ok && make_tmap_2d(&tout, a.out, 4, (uint64_t)a.G * a.N, a.K, 8, 32);
+    else
+        tout = ta;  // not used
     if (!ok) return cudaErrorInvalidValue;
     // the groups' rows are known on the device only: there at most this many tiles
     const bool known = MODE == kWeight || a.offsets == nullptr;
@@ -816,10 +861,10 @@ cudaError_t launch_tiles(Fp8ProductArgs a, cudaStream_t s) {
         cudaLaunchAttribute attr[2];
         cudaLaunchConfig_t cfg;
         split_config(&cfg, attr, a.split, (int)tiles, smem_bytes<MODE>(), s);
-        e = cudaLaunchKernelEx(&cfg, k_product<MODE, true>, ta, tb, a);
+        e = cudaLaunchKernelEx(&cfg, k_product<MODE, true>, ta, tb, tout, a);
     } else {
         e = launch_pdl(k_product<MODE, false>, dim3((unsigned)(tiles < dev.num_sms ? tiles : dev.num_sms)),
-                       dim3(THREADS), smem_bytes<MODE>(), s, ta, tb, a);
+                       dim3(THREADS), smem_bytes<MODE>(), s, ta, tb, tout, a);
     }
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -117,9 +117,10 @@ struct Work {
             const int per = n_tiles * k_tiles;
             p.g = i / per;
             const int r = i - p.g * per;
-            p.row0 = (r / n_tiles) * BM;
+            // rows first (columns first, 8192 x 4096 x 6144 took 258 us, so 252)
+            p.row0 = (r % k_tiles) * BM;
             p.nrows = BM;
-            p.col0 = (r % n_tiles) * BN;
+            p.col0 = (r / k_tiles) * BN;
             p.block0 = tt->mstart[p.g];
             p.blocks = tt->mstart[p.g + 1] - p.block0;
         } else {
@@ -245,9 +246,8 @@ __device__ __forceinline__ void promote_scaled(const uint32_t* r, float f0, floa
 // Four chunks of eight words in each of four neighbouring lanes, turned: lane j of the
 // four ends with chunk j of all four lanes, in lane order.  The accumulators hold
 // a row per lane; turned, the four lanes store 128 consecutive bytes of one row
-// at a time.  (A store of 32 bytes from each of 32 rows kept the store unit four
-// times as long: the weight gradients of 32 small experts, 369 MB, took
-// 103 us, so 85.)
+// at a time.  (A store of 32 bytes from each of 32 rows keeps the store unit four
+// times as long: a weight gradient bound by its output took 103 us so, 85 turned.)
 __device__ __forceinline__ void turn_chunks(uint32_t* v) {
     const int j = threadIdx.x & 3;
 #pragma unroll
@@ -334,7 +334,10 @@ __device__ __forceinline__ void bulk_wait() {
 // kWeight: sends a warp's 32 rows x EPI_COLS columns on their way through shared memory
 // (`buf`, two slots of eight rows), while the warp goes on to the next tile.  In
 // shared memory the rows of 32 columns lie as the tensor map's 128-byte swizzle has
-// them: 16-byte piece p of row r in place p ^ r.  A lane has row l / 4 and of each
+// them: 16-byte piece p of row r in place p ^ r.  (Stored from registers, after turning
+// chunks among four lanes, 32 experts of 2048 x 1408 over 5003 rows, 369 MB of output,
+// took 84.0 us, so 78.5; without the L2 policy 80.  The bytes alone take 50 us as a
+// fill, 56 at the copy's rate.)  A lane has row l / 4 and of each
 // eight columns a pair; odd rows take the groups of eight in another order, so that
 // the stores of half a warp fall on distinct banks.
 __device__ __forceinline__ void send_tile(const Fp8ProductArgs& a, const CUtensorMap* map, uint32_t buf,
@@ -369,11 +372,15 @@ __device__ __forceinline__ void send_tile(const Fp8ProductArgs& a, const CUtenso
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
+            uint64_t first_out;  // the operands stay in L2 rather than the output
+            asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(first_out));
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
-                             "r"(col + 32 * h), "r"((int)(row0 + 8 * q)), "r"(slot + h * OUT_ATOM)
-                             : "memory");
+                asm volatile(
+                    "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group.L2::cache_hint "
+                    "[%0, {%1, %2}], [%3], %4;" ::"l"(map),
+                    "r"(col + 32 * h), "r"((int)(row0 + 8 * q)), "r"(slot + h * OUT_ATOM), "l"(first_out)
+                    : "memory");
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
     }
@@ -477,9 +484,9 @@ __device__ __forceinline__ void add_tiles(const Fp8ProductArgs& a, const Smem& s
 // commit, wait, TMEM loads, products, arrival, next issue.  Cycles per block of a
 // 128 x 256 tile: 815 in all, 720 without the MMAs, 613 without the promotion,
 // 520 with neither.  At large sizes the power limit levels what is left of the
-// difference: 8192 x 4096 x 6144 takes 180 us (2.29 PFLOP/s) at ~1.5 GHz, 143 us
+// difference: 8192 x 4096 x 6144 takes 177 us (2.33 PFLOP/s) at ~1.5 GHz, 143 us
 // without its promotion, and variants with 5% fewer cycles took the same time
-// at a lower clock.  The weight gradient (two products a value) takes 260 us,
+// at a lower clock.  The weight gradient (two products a value) takes 252 us,
 // 4096 x 6144 x 2048 rows of the input gradient 52 us, 32 groups of 8192 rows 280
 // us (their 805 MB of weights alone 123 us; the groups' last tiles pad 336
 // tiles of rows to 432).

@@ -96,6 +96,19 @@ def test_against_formula(case, mask, renorm):
     assert M.read_device_status(o["ws"]) == M.OK
 
 
+@pytest.mark.parametrize("T,E,k", [(37, 256, 8), (5003, 60, 4), (9500, 129, 7)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gradient_in_place(T, E, k, renorm):
+    """dlogits may be the logits' own buffer: the same bits as into another one."""
+    c = {n: dev(v) if isinstance(v, torch.Tensor) else v for n, v in make(T, E, k, T, renorm, 0.8).items()}
+    o = outputs(T, E)
+    run(c, o)
+    apart = o["dlogits"].clone()
+    o["dlogits"] = c["logits"]
+    run(c, o)
+    assert torch.equal(c["logits"], apart)
+
+
 @pytest.mark.parametrize("weights,loss", [(True, False), (False, True)])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_one_part_alone(weights, loss, renorm):

@@ -554,7 +554,7 @@ int64_t moe_fp8_token_rows(int32_t M, int32_t G);
  * moe_gemm_fp8) follow one another, each group's padded with zero codes to a
  * multiple of 128; each column's 128 codes of one block share s = fp32(amax)/448
  * (1 for zeros), q = e4m3_rne_satfinite(fp32(x / s)).  What lies behind the last
- * group's last block is not written.  x, q_t 16-byte aligned. */
+ * group's last block is not written.  x, q_t 16-byte aligned; R <= 128 * 65535. */
 moe_status moe_quantize_fp8_tokens(const uint16_t* x, const int32_t* offsets, int32_t G, int32_t M,
                                    int32_t cols, uint8_t* q_t, float* scale_t, void* stream);
 
@@ -564,7 +564,8 @@ moe_status moe_quantize_fp8_tokens(const uint16_t* x, const int32_t* offsets, in
  * (b: the blocks of group g), dy_t [N][R] and x_t [K][R] as
  * moe_quantize_fp8_tokens writes them for the same offsets and M.  dw [G][N][K]
  * f32, added to when accumulate != 0, else written (zeros for a group without
- * rows).  Limits as moe_gemm_fp8. */
+ * rows).  Limits as moe_gemm_fp8, and R <= 128 * 65535; dy_t, x_t, dw 16-byte
+ * aligned. */
 moe_status moe_gemm_fp8_wgrad(const uint8_t* dy_t, const float* dy_t_scale, const uint8_t* x_t,
                               const float* x_t_scale, const int32_t* offsets, int32_t G, int32_t M,
                               int32_t N, int32_t K, float* dw, int32_t accumulate, void* ws,

@@ -15,9 +15,9 @@
 // or 8 CTAs; each leaves its FP32 tile in its shared memory, and every CTA adds a
 // share of the rows over the cluster, in rank order (deterministic).
 //
-// Measured: 1 x 6144 x 2048 6.2 us, 1 x 4096 x 6144 7.8 us (the 128 x 256 tiles 23.5),
-// 64 x 4096 x 6144 9.8 us, the input gradient 64 x 6144 x 2048 8.7 us, and 1 x 8192 x
-// 8192 15.0 us (67 MB, 4.5 TB/s).  At the small sizes the weights' bytes would
+// Measured: 1 x 6144 x 2048 5.9 us, 1 x 4096 x 6144 7.6 us (the 128 x 256 tiles 23.5),
+// 64 x 4096 x 6144 9.7 us, the input gradient 64 x 6144 x 2048 8.3 us, and 1 x 8192 x
+// 8192 14.6 us (67 MB, 4.6 TB/s).  At the small sizes the weights' bytes would
 // take 2 to 4 us: the rest is the launch, the first load's latency and the
 // cluster's exchange.
 #include <atomic>

@@ -352,6 +352,70 @@ def test_capture_and_replay_on_a_side_stream():
         assert torch.equal(a[k], fresh[k]) and torch.equal(b[k], eager_b[k]), k
 
 
+# rows of each group, N, K: the persistent tiles and their bulk stores, and sums split
+# over clusters
+ACCUMULATED = [([700], 1024, 5120), ([0, 300, 129, 5], 512, 640), ([4500], 384, 640), ([40] * 30, 640, 768)]
+
+
+@pytest.mark.parametrize("case", range(len(ACCUMULATED)))
+def test_accumulation_in_a_row(case):
+    """Weight gradients added into one buffer by launches that follow one another, eager
+    and replayed: each adds the same bits with one rounding."""
+    sizes, N, K = ACCUMULATED[case]
+    rows, off = make_groups(sizes, 0, 0)
+    G, R = len(sizes), M.fp8_token_rows(rows, len(sizes))
+    off = off.to(DEV)
+    ops = []
+    for i, c in enumerate((N, K)):
+        q = torch.zeros((c, R), dtype=torch.uint8, device=DEV)
+        s = torch.zeros((R // 128, c), device=DEV)
+        M.quantize_fp8_tokens(randn((rows, c), 11 + i).to(DEV), off, q, s)
+        ops += [q, s]
+    dw, w = torch.empty((G, N, K), device=DEV), workspace()
+    M.gemm_fp8_wgrad(*ops, off, rows, dw, False, w)
+    one = dw.clone()
+    for _ in range(3):
+        M.gemm_fp8_wgrad(*ops, off, rows, dw, True, w)
+    want = ((one + one) + one) + one
+    assert torch.equal(dw, want)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        for _ in range(2):
+            M.gemm_fp8_wgrad(*ops, off, rows, dw, True, w)
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        want = want + one
+    assert torch.equal(dw, want) and M.read_device_status(w) == M.OK
+
+
+def test_two_streams_of_weight_gradients():
+    """Split sums and persistent tiles in flight together, a workspace each."""
+    shapes = [(4500, 384, 640), (600, 1024, 4096)]
+    calls = []
+    for i, (rows, N, K) in enumerate(shapes):
+        R = M.fp8_token_rows(rows)
+        ops = []
+        for j, c in enumerate((N, K)):
+            q = torch.zeros((c, R), dtype=torch.uint8, device=DEV)
+            s = torch.zeros((R // 128, c), device=DEV)
+            M.quantize_fp8_tokens(randn((rows, c), 5 * i + j).to(DEV), None, q, s)
+            ops += [q, s]
+        alone = torch.empty((N, K), device=DEV)
+        M.gemm_fp8_wgrad(*ops, None, rows, alone, False, workspace())
+        calls.append((ops, rows, alone, torch.empty_like(alone), workspace(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for ops, rows, _, out, w, st in calls:
+            M.gemm_fp8_wgrad(*ops, None, rows, out, False, w, st)
+    torch.cuda.synchronize()
+    for _, _, alone, out, w, _ in calls:
+        assert torch.equal(out, alone) and M.read_device_status(w) == M.OK
+
+
 def test_two_streams_at_once():
     """Two products in flight on two streams (a workspace each) give the bits of one."""
     rows, N, K = 600, 640, 512

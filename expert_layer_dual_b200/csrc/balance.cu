@@ -236,6 +236,9 @@ __global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(1024)
     __shared__ int s_tokens[32], s_bad[32];
     __shared__ double s_term[32], s_share[kFinishBlocks];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // A block's shared memory may be reached once it is known to run: every block arrives
+    // here and waits before the exchange, when all of them long have.
+    cluster_arrive();
     pdl_trigger();
     pdl_wait();
     const int e = blockIdx.x * 32 + lane;
@@ -287,6 +290,7 @@ __global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(1024)
         s_term[warp] = mine < E ? (double)m * E * inv * mean : 0.0;
     }
     __syncthreads();
+    cluster_wait();
     if (warp == 0) {
         double term = s_term[lane];
 #pragma unroll

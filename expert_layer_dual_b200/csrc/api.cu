@@ -1031,10 +1031,37 @@ moe_status check_product(const int32_t* offsets, int32_t G, int32_t M, int32_t N
     return MOE_OK;
 }
 
+// Fields common to the three products.
+Fp8ProductArgs product_args(const uint8_t* a, const float* a_scale, const uint8_t* b, const float* b_scale,
+                            const int32_t* offsets, int32_t G, int32_t M, int32_t N, int32_t K, void* out,
+                            int32_t out_type, void* ws) {
+    Fp8ProductArgs p{};
+    p.a = a;
+    p.a_scale = a_scale;
+    p.b = b;
+    p.b_scale = b_scale;
+    p.offsets = offsets;
+    p.G = G;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.out = out;
+    p.out_type = out_type;
+    p.status = at<int32_t>(ws, 0);
+    p.timeout_ns = kDefaultTimeoutNs;
+    return p;
+}
+
+// A bound of the waits and a block that gives up, for moe_selftest_product_timeout.
+struct GiveUp {
+    uint64_t timeout_ns;
+    uint32_t block;
+};
+
 moe_status run_product(bool forward, const uint8_t* a, const float* a_scale, const uint8_t* w,
                        const float* w_scale, const int32_t* offsets, int32_t G, int32_t M, int32_t N,
                        int32_t K, void* out, int32_t out_type, void* ws, size_t ws_bytes,
-                       void* stream) {
+                       void* stream, const GiveUp* give_up = nullptr) {
     moe_status r = check_product(offsets, G, M, N, K);
     if (r != MOE_OK) return r;
     if (out_type != MOE_OUT_BF16 && out_type != MOE_OUT_F16 && out_type != MOE_OUT_F32)
@@ -1045,21 +1072,40 @@ moe_status run_product(bool forward, const uint8_t* a, const float* a_scale, con
         return MOE_ERR_INVALID_ARG;
     if ((r = check_ws(ws, ws_bytes, kWsHeader)) != MOE_OK) return r;
     if (!device_ok()) return MOE_ERR_UNSUPPORTED;
-    Fp8ProductArgs p{};
-    p.a = a;
-    p.a_scale = a_scale;
-    p.b = w;
-    p.b_scale = w_scale;
-    p.offsets = offsets;
-    p.G = G;
-    p.M = M;
-    p.N = N;
-    p.K = K;
-    p.out = out;
-    p.out_type = out_type;
-    p.status = at<int32_t>(ws, 0);
-    p.timeout_ns = kDefaultTimeoutNs;
+    Fp8ProductArgs p = product_args(a, a_scale, w, w_scale, offsets, G, M, N, K, out, out_type, ws);
+    if (give_up != nullptr) {
+        p.timeout_ns = give_up->timeout_ns;
+        p.give_up = give_up->block + 1;
+    }
     return cuda_status((forward ? launch_gemm_fp8 : launch_gemm_fp8_dgrad)(p, as_stream(stream)));
+}
+
+moe_status run_wgrad(const uint8_t* dy_t, const float* dy_t_scale, const uint8_t* x_t, const float* x_t_scale,
+                     const int32_t* offsets, int32_t G, int32_t M, int32_t N, int32_t K, float* dw,
+                     int32_t accumulate, void* ws, size_t ws_bytes, void* stream,
+                     const GiveUp* give_up = nullptr) {
+    moe_status r = check_product(offsets, G, M, N, K);
+    if (r != MOE_OK) return r;
+    if (dw == nullptr || !aligned16(dw)) return MOE_ERR_INVALID_ARG;
+    if (M > 0 && (dy_t == nullptr || dy_t_scale == nullptr || x_t == nullptr || x_t_scale == nullptr ||
+                  !aligned16(dy_t) || !aligned16(x_t)))
+        return MOE_ERR_INVALID_ARG;
+    if ((r = check_ws(ws, ws_bytes, kWsHeader)) != MOE_OK) return r;
+    if (fp8_token_rows(M, G) / 128 > 65535) return MOE_ERR_UNSUPPORTED;
+    if (!device_ok()) return MOE_ERR_UNSUPPORTED;
+    if (M == 0) {  // the operands are empty: nothing to add, or zeros
+        if (accumulate) return MOE_OK;
+        return cuda_status(cudaMemsetAsync(dw, 0, (size_t)G * N * K * 4, as_stream(stream)));
+    }
+    Fp8ProductArgs p =
+        product_args(dy_t, dy_t_scale, x_t, x_t_scale, offsets, G, M, N, K, dw, MOE_OUT_F32, ws);
+    p.rows_t = fp8_token_rows(M, G);
+    p.accumulate = accumulate != 0 ? 1 : 0;
+    if (give_up != nullptr) {
+        p.timeout_ns = give_up->timeout_ns;
+        p.give_up = give_up->block + 1;
+    }
+    return cuda_status(launch_gemm_fp8_wgrad(p, as_stream(stream)));
 }
 }  // namespace
 
@@ -1099,36 +1145,19 @@ moe_status moe_gemm_fp8_wgrad(const uint8_t* dy_t, const float* dy_t_scale, cons
                               const float* x_t_scale, const int32_t* offsets, int32_t G, int32_t M,
                               int32_t N, int32_t K, float* dw, int32_t accumulate, void* ws,
                               size_t ws_bytes, void* stream) {
-    moe_status r = check_product(offsets, G, M, N, K);
-    if (r != MOE_OK) return r;
-    if (dw == nullptr || !aligned16(dw)) return MOE_ERR_INVALID_ARG;
-    if (M > 0 && (dy_t == nullptr || dy_t_scale == nullptr || x_t == nullptr || x_t_scale == nullptr ||
-                  !aligned16(dy_t) || !aligned16(x_t)))
-        return MOE_ERR_INVALID_ARG;
-    if ((r = check_ws(ws, ws_bytes, kWsHeader)) != MOE_OK) return r;
-    if (fp8_token_rows(M, G) / 128 > 65535) return MOE_ERR_UNSUPPORTED;
-    if (!device_ok()) return MOE_ERR_UNSUPPORTED;
-    if (M == 0) {  // the operands are empty: nothing to add, or zeros
-        if (accumulate) return MOE_OK;
-        return cuda_status(cudaMemsetAsync(dw, 0, (size_t)G * N * K * 4, as_stream(stream)));
-    }
-    Fp8ProductArgs p{};
-    p.a = dy_t;
-    p.a_scale = dy_t_scale;
-    p.b = x_t;
-    p.b_scale = x_t_scale;
-    p.offsets = offsets;
-    p.G = G;
-    p.M = M;
-    p.N = N;
-    p.K = K;
-    p.rows_t = fp8_token_rows(M, G);
-    p.out = dw;
-    p.out_type = MOE_OUT_F32;
-    p.accumulate = accumulate != 0 ? 1 : 0;
-    p.status = at<int32_t>(ws, 0);
-    p.timeout_ns = kDefaultTimeoutNs;
-    return cuda_status(launch_gemm_fp8_wgrad(p, as_stream(stream)));
+    return run_wgrad(dy_t, dy_t_scale, x_t, x_t_scale, offsets, G, M, N, K, dw, accumulate, ws, ws_bytes, stream);
+}
+
+moe_status moe_selftest_product_timeout(int32_t op, const uint8_t* a, const float* a_scale, const uint8_t* b,
+                                        const float* b_scale, int32_t M, int32_t N, int32_t K, float* out,
+                                        int32_t accumulate, int32_t block, int32_t limit_us, void* ws,
+                                        size_t ws_bytes, void* stream) {
+    if (op < 0 || op > 2 || block < 0 || limit_us <= 0 || limit_us > 1000000) return MOE_ERR_INVALID_ARG;
+    const GiveUp g{(uint64_t)limit_us * 1000ull, (uint32_t)block};
+    if (op == 2)
+        return run_wgrad(a, a_scale, b, b_scale, nullptr, 1, M, N, K, out, accumulate, ws, ws_bytes, stream, &g);
+    return run_product(op == 0, a, a_scale, b, b_scale, nullptr, 1, M, N, K, out, MOE_OUT_F32, ws, ws_bytes, stream,
+                       &g);
 }
 
 moe_status moe_read_device_status(const void* ws, void* stream) {

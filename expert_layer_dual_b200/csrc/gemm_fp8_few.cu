@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         const CUtensorMap* map = is_w ? &tm_w : &tm_x;
         Ring<STAGES> st;
         uint32_t issued = 0;
+        const uint32_t never = is_w && blockIdx.x + 1 == a.give_up;  // the self-test's wait
         bool ok = true;
         for (int i = first; ok && i < total; i += step) {
             const Tile t = decode_tile(sm.tt, a.G, n_tiles, i, FN);
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (INPUT) x = t.n * FM;
             }
             for (int kb = 0; kb < blocks; ++kb, st.next()) {
-                if (!warp_wait_phase(sm.done(st.slot), st.round ^ 1u, a.timeout_ns, sm.abort_flag())) {
+                if (!warp_wait_phase(sm.done(st.slot), st.round ^ 1u ^ never, a.timeout_ns, sm.abort_flag())) {
                     ok = false;
                     break;
                 }

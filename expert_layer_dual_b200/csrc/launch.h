@@ -246,6 +246,7 @@ struct Fp8ProductArgs {
     int split;               // CTAs of a cluster that share a 128 x 256 tile
     int32_t* status;
     uint64_t timeout_ns;
+    uint32_t give_up;        // 1 + the block whose first load waits for what never comes (self-test); 0: none
 };
 cudaError_t launch_gemm_fp8(const Fp8ProductArgs& a, cudaStream_t s);
 cudaError_t launch_gemm_fp8_dgrad(const Fp8ProductArgs& a, cudaStream_t s);

@@ -62,7 +62,7 @@ EXPORTS = ["moe_status_string", "moe_workspace_bytes", "moe_permute_workspace_by
            "moe_peer_buffer_close", "moe_peer_buffer_free",
            "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_backward",
            "moe_gemm_fp8", "moe_gemm_fp8_dgrad", "moe_fp8_token_rows", "moe_quantize_fp8_tokens",
-           "moe_gemm_fp8_wgrad"]
+           "moe_gemm_fp8_wgrad", "moe_selftest_product_timeout"]
 OUT_BF16, OUT_F16, OUT_F32 = range(3)
 
 
@@ -143,6 +143,8 @@ _sig = {
     "moe_quantize_fp8_tokens": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]),
     "moe_gemm_fp8_wgrad": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _sz,
                                   _vp]),
+    "moe_selftest_product_timeout": (_i32, [_i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _i32,
+                                            _i32, _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _sig.items():
     _f = getattr(_lib, _name)
@@ -545,6 +547,18 @@ def read_device_status(ws, stream=None) -> int:
 
 def selftest_timeout(ws, limit_us: int, stream=None):
     _check(_lib.moe_selftest_timeout(_p(ws), int(limit_us), _stream(stream)), "moe_selftest_timeout")
+
+
+def selftest_product_timeout(op: int, a, a_s, b, b_s, M: int, out, accumulate, block: int, limit_us: int, ws,
+                             stream=None):
+    """moe_selftest_product_timeout: the operands of gemm_fp8 (op 0), gemm_fp8_dgrad (1) or
+    gemm_fp8_wgrad (2) for one group; out float32, [M, N], [M, K] or [N, K]."""
+    if out.dtype != torch.float32:
+        raise ValueError(f"out: {out.dtype}; expected float32")
+    N, K = out.shape if op == 2 else b.shape
+    _check(_lib.moe_selftest_product_timeout(op, _p(a), _p(a_s), _p(b), _p(b_s), M, N, K, _p(out), int(accumulate),
+                                             int(block), int(limit_us), _p(ws), ws.numel() * ws.element_size(),
+                                             _stream(stream)), "moe_selftest_product_timeout")
 
 
 # ------------------------------------------------------------------ layer object

@@ -571,6 +571,17 @@ moe_status moe_gemm_fp8_wgrad(const uint8_t* dy_t, const float* dy_t_scale, cons
                               int32_t N, int32_t K, float* dw, int32_t accumulate, void* ws,
                               size_t ws_bytes, void* stream);
 
+/* Self-test of the FP8 products' failure path: runs the product (op 0:
+ * moe_gemm_fp8, 1: moe_gemm_fp8_dgrad, 2: moe_gemm_fp8_wgrad; one group, FP32
+ * output) with waits bounded by limit_us (at most 1 s), the first load of its
+ * thread block `block` waiting for a signal that never comes.  Records
+ * MOE_ERR_DEVICE_TIMEOUT in ws's status word; the output tiles of that block, and of
+ * the blocks that share them, are left as they were, the others are written. */
+moe_status moe_selftest_product_timeout(int32_t op, const uint8_t* a, const float* a_scale,
+                                        const uint8_t* b, const float* b_scale, int32_t M, int32_t N,
+                                        int32_t K, float* out, int32_t accumulate, int32_t block,
+                                        int32_t limit_us, void* ws, size_t ws_bytes, void* stream);
+
 /* Synchronises `stream` and returns the device status word of `ws`
  * (MOE_OK, MOE_ERR_DEVICE_TIMEOUT or MOE_ERR_DEVICE_BAD_INDEX). */
 moe_status moe_read_device_status(const void* ws, void* stream);

@@ -10,7 +10,7 @@ import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "expert_layer_dual_b200", "csrc")
 # what reaches another CTA of the cluster, or calls a helper that does
-REMOTE = re.compile(r"\b(smem_in_rank|in_rank|arrive_cluster|mbar_arrive_cluster|add_tiles|add_rows|"
+REMOTE = re.compile(r"\b(smem_in_rank|in_rank|arrive_cluster|mbar_arrive_cluster|add_tiles|add_rows|share_failed|"
                     r"warp_arrive_leader|tma_load_2d_pair)\s*[(<]|st\.shared::cluster|ld\.shared::cluster|mapa\.")
 # prologue and teardown: the pair kernels' helpers, which hold their cluster_sync
 PASSED = re.compile(r"\b(cluster_sync|cluster_wait|prologue|teardown)\s*\(")

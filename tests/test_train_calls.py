@@ -1,0 +1,32 @@
+"""The training entry points' calls on the CPU: refusals, and what the native binding does
+around a call.  Nothing is launched: there is no device, or the call is refused before."""
+import ctypes
+
+import pytest
+import torch
+
+P = ctypes.c_void_p
+OKP = 1 << 20          # an aligned address; nothing is launched without a device
+
+
+@pytest.fixture(scope="module")
+def M():
+    import expert_layer_dual_b200.moe as moe
+    return moe
+
+
+@pytest.mark.parametrize("change,code", [
+    ({"op": 3}, 1), ({"op": -1}, 1), ({"block": -1}, 1), ({"limit": 0}, 1), ({"limit": 1000001}, 1), ({"N": 100}, 2),
+    ({"a": None}, 1), ({"out": OKP + 4}, 1), ({"ws": None}, 1), ({"ws_bytes": 128}, 4), ({"op": 2, "M": 9000000}, 2)])
+def test_selftest_refusals(M, change, code):
+    a = {"op": 0, "a": OKP, "a_s": OKP, "b": OKP, "b_s": OKP, "M": 5, "N": 256, "K": 128, "out": OKP, "block": 0,
+         "limit": 100, "ws": OKP, "ws_bytes": 256, **change}
+    assert M._lib.moe_selftest_product_timeout(
+        a["op"], P(a["a"]), P(a["a_s"]), P(a["b"]), P(a["b_s"]), a["M"], a["N"], a["K"], P(a["out"]), 0, a["block"],
+        a["limit"], P(a["ws"]), a["ws_bytes"], None) == code
+
+
+def test_selftest_takes_fp32_outputs_only(M):
+    z = torch.zeros((128, 128), dtype=torch.uint8)
+    with pytest.raises(ValueError, match="float32"):
+        M.selftest_product_timeout(0, z, z, z, z, 128, torch.zeros((128, 128), dtype=torch.bfloat16), False, 0, 100, z)

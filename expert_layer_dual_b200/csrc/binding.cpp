@@ -91,6 +91,8 @@ struct Args {
     static bool i32(at::ScalarType s) { return s == at::kInt; }
     static bool codes(at::ScalarType s) { return s == at::kByte || s == at::kFloat8_e4m3fn; }
     static bool bf16(at::ScalarType s) { return s == at::kBFloat16 || s == at::kUInt16; }
+    static bool halves(at::ScalarType s) { return bf16(s) || s == at::kShort; }
+    static bool bytes(at::ScalarType s) { return codes(s) || s == at::kChar; }
     static bool flags(at::ScalarType s) { return s == at::kByte || s == at::kBool; }
     static bool output(at::ScalarType s) { return bf16(s) || s == at::kHalf || s == at::kFloat; }
 
@@ -128,6 +130,14 @@ struct Args {
         }
         if (bytes != nullptr) *bytes = t->nbytes();
         return t->const_data_ptr();
+    }
+    // Tensor i has to hold `elements` or more of one of the types, in any shape.
+    template <typename Type>
+    void room(int i, const char* name, Type is_type, const char* type_name, int64_t elements) {
+        const at::Tensor* t = tensor(i, name);
+        if (t == nullptr || (is_type(t->scalar_type()) && t->numel() >= elements)) return;
+        const std::string want = c10::str(elements, " elements or more of ", type_name);
+        refuse(name, *t, want.c_str());
     }
     void* workspace(int i, size_t* bytes) { return const_cast<void*>(buffer(i, "workspace", bytes)); }
     static bool fits_int(std::initializer_list<int64_t> v) {
@@ -236,12 +246,15 @@ PyObject* product(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                                                 c.stream));
 }
 
-// (dev, stream, x, codes, scales): x gives the sizes; as before this binding, the
-// buffers' shapes and types are the caller's.
+// (dev, stream, x, codes, scales): x gives the sizes; the buffers may have any shape, and
+// hold more than is written.
 PyObject* quantize_act(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args c;
     int64_t M, cols;
     if (!c.open(args, n, 5) || !c.matrix(2, "x", &M, &cols)) return nullptr;
+    c.room(2, "x", Args::halves, "bfloat16, uint16 or int16", M * cols);
+    c.room(3, "codes", Args::bytes, "uint8, int8 or float8_e4m3fn", M * cols);
+    c.room(4, "scales", Args::f32, "float32", M * (cols / 128));
     const void* x = c.buffer(2, "x");
     void* q = const_cast<void*>(c.buffer(3, "codes"));
     void* s = const_cast<void*>(c.buffer(4, "scales"));

@@ -345,6 +345,9 @@ def quantize_weights_fp8(W, q, scale, stream=None):
 
 
 def quantize_act_fp8(x, q, scale, stream=None):
+    """moe_quantize_act_fp8: x [rows, cols] (bf16, or its bits as uint16 or int16) -> rows * cols
+    codes in q (a byte each) and rows * cols / 128 scales in scale (f32), which may have any
+    shape and hold more."""
     dev = _launch_device(x)
     _check(_native.quantize_act_fp8(dev, _stream(stream, dev), x, q, scale), "moe_quantize_act_fp8")
 

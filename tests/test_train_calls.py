@@ -30,3 +30,21 @@ def test_selftest_takes_fp32_outputs_only(M):
     z = torch.zeros((128, 128), dtype=torch.uint8)
     with pytest.raises(ValueError, match="float32"):
         M.selftest_product_timeout(0, z, z, z, z, 128, torch.zeros((128, 128), dtype=torch.bfloat16), False, 0, 100, z)
+
+
+@pytest.mark.parametrize("change,want", [
+    ({"x": torch.zeros((4, 256), dtype=torch.float16)}, "1024 elements or more of bfloat16"),
+    ({"x": torch.zeros((4, 256))}, "of bfloat16"),
+    ({"q": torch.zeros((4, 255), dtype=torch.uint8)}, "1024 elements or more of uint8"),
+    ({"q": torch.zeros((4, 256), dtype=torch.bfloat16)}, "of uint8"),
+    ({"q": torch.zeros((0, 256), dtype=torch.uint8)}, "of uint8"),
+    ({"s": torch.zeros((4, 1))}, "8 elements or more of float32"),
+    ({"s": torch.zeros((4, 2), dtype=torch.float64)}, "of float32"),
+    ({"s": torch.zeros((8,), dtype=torch.bfloat16)}, "of float32")])
+def test_row_quantiser_checks_types_and_room(M, change, want):
+    """A buffer that is too small would be written past its end on the device, values of
+    another type read as bf16 bits."""
+    a = {"x": torch.zeros((4, 256), dtype=torch.bfloat16), "q": torch.zeros((4, 256), dtype=torch.uint8),
+         "s": torch.zeros((4, 2)), **change}
+    with pytest.raises(ValueError, match=want):
+        M._native.quantize_act_fp8(0, 0, a["x"], a["q"], a["s"])

@@ -1148,6 +1148,16 @@ moe_status moe_gemm_fp8_wgrad(const uint8_t* dy_t, const float* dy_t_scale, cons
     return run_wgrad(dy_t, dy_t_scale, x_t, x_t_scale, offsets, G, M, N, K, dw, accumulate, ws, ws_bytes, stream);
 }
 
+void* moe_device_address(const void* p) {
+    cudaPointerAttributes at{};
+    if (p == nullptr) return nullptr;
+    if (cudaPointerGetAttributes(&at, p) != cudaSuccess) {
+        cudaGetLastError();  // not sticky: an address unknown to the driver, or no device
+        return nullptr;
+    }
+    return at.devicePointer;
+}
+
 moe_status moe_selftest_product_timeout(int32_t op, const uint8_t* a, const float* a_scale, const uint8_t* b,
                                         const float* b_scale, int32_t M, int32_t N, int32_t K, float* out,
                                         int32_t accumulate, int32_t block, int32_t limit_us, void* ws,

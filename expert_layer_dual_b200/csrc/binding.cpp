@@ -131,13 +131,25 @@ struct Args {
         if (bytes != nullptr) *bytes = t->nbytes();
         return t->const_data_ptr();
     }
-    // Tensor i has to hold `elements` or more of one of the types, in any shape.
+    // Tensor i has to hold `elements` or more of one of the types, in any shape (None: none).
     template <typename Type>
     void room(int i, const char* name, Type is_type, const char* type_name, int64_t elements) {
+        if (none(i) && elements == 0) return;
         const at::Tensor* t = tensor(i, name);
         if (t == nullptr || (is_type(t->scalar_type()) && t->numel() >= elements)) return;
         const std::string want = c10::str(elements, " elements or more of ", type_name);
         refuse(name, *t, want.c_str());
+    }
+    // The address of a contiguous tensor that the current device reaches: its own memory,
+    // pinned host memory, another device's with peer access; NULL for an empty one.
+    const void* reachable(int i, const char* name) {
+        if (none(i)) return nullptr;
+        const at::Tensor* t = tensor(i, name);
+        if (t == nullptr || t->numel() == 0) return nullptr;
+        if (t->is_cuda() && t->get_device() == dev) return buffer(i, name);
+        const void* p = t->is_contiguous() ? moe_device_address(t->const_data_ptr()) : nullptr;
+        if (p == nullptr) refuse(name, *t, "a buffer that the device reaches");
+        return p;
     }
     void* workspace(int i, size_t* bytes) { return const_cast<void*>(buffer(i, "workspace", bytes)); }
     static bool fits_int(std::initializer_list<int64_t> v) {
@@ -246,8 +258,8 @@ PyObject* product(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                                                 c.stream));
 }
 
-// (dev, stream, x, codes, scales): x gives the sizes; the buffers may have any shape, and
-// hold more than is written.
+// (dev, stream, x, codes, scales): x gives the sizes; the buffers may have any shape, hold
+// more than is written, and lie in any memory that the device reaches.
 PyObject* quantize_act(PyObject*, PyObject* const* args, Py_ssize_t n) {
     Args c;
     int64_t M, cols;
@@ -255,9 +267,9 @@ PyObject* quantize_act(PyObject*, PyObject* const* args, Py_ssize_t n) {
     c.room(2, "x", Args::halves, "bfloat16, uint16 or int16", M * cols);
     c.room(3, "codes", Args::bytes, "uint8, int8 or float8_e4m3fn", M * cols);
     c.room(4, "scales", Args::f32, "float32", M * (cols / 128));
-    const void* x = c.buffer(2, "x");
-    void* q = const_cast<void*>(c.buffer(3, "codes"));
-    void* s = const_cast<void*>(c.buffer(4, "scales"));
+    const void* x = c.reachable(2, "x");
+    void* q = const_cast<void*>(c.reachable(3, "codes"));
+    void* s = const_cast<void*>(c.reachable(4, "scales"));
     if (!c.ok) return nullptr;
     if (!Args::fits_int({cols})) return PyLong_FromLong(MOE_ERR_UNSUPPORTED);
     return c.status(moe_quantize_act_fp8(static_cast<const uint16_t*>(x), M, (int32_t)cols,

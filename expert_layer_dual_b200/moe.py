@@ -62,7 +62,7 @@ EXPORTS = ["moe_status_string", "moe_workspace_bytes", "moe_permute_workspace_by
            "moe_peer_buffer_close", "moe_peer_buffer_free",
            "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_backward",
            "moe_gemm_fp8", "moe_gemm_fp8_dgrad", "moe_fp8_token_rows", "moe_quantize_fp8_tokens",
-           "moe_gemm_fp8_wgrad", "moe_selftest_product_timeout"]
+           "moe_gemm_fp8_wgrad", "moe_selftest_product_timeout", "moe_device_address"]
 OUT_BF16, OUT_F16, OUT_F32 = range(3)
 
 
@@ -143,6 +143,7 @@ _sig = {
     "moe_quantize_fp8_tokens": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp]),
     "moe_gemm_fp8_wgrad": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp, _sz,
                                   _vp]),
+    "moe_device_address": (_vp, [_vp]),
     "moe_selftest_product_timeout": (_i32, [_i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _i32, _i32,
                                             _i32, _vp, _sz, _vp]),
 }
@@ -347,9 +348,11 @@ def quantize_weights_fp8(W, q, scale, stream=None):
 def quantize_act_fp8(x, q, scale, stream=None):
     """moe_quantize_act_fp8: x [rows, cols] (bf16, or its bits as uint16 or int16) -> rows * cols
     codes in q (a byte each) and rows * cols / 128 scales in scale (f32), which may have any
-    shape and hold more."""
-    dev = _launch_device(x)
-    _check(_native.quantize_act_fp8(dev, _stream(stream, dev), x, q, scale), "moe_quantize_act_fp8")
+    shape and hold more.  The tensors may lie in any memory that the current device reaches,
+    pinned host memory among it."""
+    dev = _current_device() if torch.cuda.is_initialized() else -1
+    _check(_native.quantize_act_fp8(dev, _stream(stream, None if dev < 0 else dev), x, q, scale),
+           "moe_quantize_act_fp8")
 
 
 def quantize_weights_mxfp8(W, q, scale, stream=None):

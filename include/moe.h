@@ -571,6 +571,11 @@ moe_status moe_gemm_fp8_wgrad(const uint8_t* dy_t, const float* dy_t_scale, cons
                               int32_t N, int32_t K, float* dw, int32_t accumulate, void* ws,
                               size_t ws_bytes, void* stream);
 
+/* The address by which the current device reaches `p` directly: device memory (another
+ * device's with peer access enabled among it), pinned or managed host memory; NULL
+ * where it does not.  Launches nothing. */
+void* moe_device_address(const void* p);
+
 /* Self-test of the FP8 products' failure path: runs the product (op 0:
  * moe_gemm_fp8, 1: moe_gemm_fp8_dgrad, 2: moe_gemm_fp8_wgrad; one group, FP32
  * output) with waits bounded by limit_us (at most 1 s), the first load of its

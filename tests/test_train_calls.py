@@ -48,3 +48,19 @@ def test_row_quantiser_checks_types_and_room(M, change, want):
          "s": torch.zeros((4, 2)), **change}
     with pytest.raises(ValueError, match=want):
         M._native.quantize_act_fp8(0, 0, a["x"], a["q"], a["s"])
+
+
+def test_row_quantiser_takes_empty_tensors_of_any_device(M):
+    """No rows: nothing is read or written, so nothing is asked of the buffers."""
+    q, s = torch.zeros((0, 256), dtype=torch.uint8), torch.zeros((0, 2))
+    for x in (torch.zeros((0, 256), dtype=torch.bfloat16), torch.zeros((0, 256), dtype=torch.int16)):
+        assert M._native.quantize_act_fp8(0, 0, x, q, s) == M.OK
+        assert M._native.quantize_act_fp8(-1, 0, x, None, None) == M.OK
+        M.quantize_act_fp8(x, q, s, stream=0)
+
+
+def test_row_quantiser_refuses_memory_that_the_device_does_not_reach(M):
+    x, q, s = torch.zeros((4, 256), dtype=torch.bfloat16), torch.zeros((4, 256), dtype=torch.uint8), torch.zeros((4, 2))
+    assert M._lib.moe_device_address(x.data_ptr()) is None
+    with pytest.raises(ValueError, match="reaches"):
+        M.quantize_act_fp8(x, q, s, stream=0)

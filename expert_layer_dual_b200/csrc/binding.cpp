@@ -157,7 +157,23 @@ struct Args {
             if (x < 0 || x > INT32_MAX) return false;
         return true;
     }
-    PyObject* status(moe_status s) { return ok ? PyLong_FromLong(s) : nullptr; }
+    // The entry point's status, called without the interpreter lock: a launch waits while the
+    // stream's queue is full, and what empties it may be a Python callback in the stream.
+    // The tensors stay alive: the caller holds the arguments.
+    template <typename Call>
+    PyObject* status(Call call) {
+        if (!ok) return nullptr;
+        struct Unlocked {
+            PyThreadState* thread = PyEval_SaveThread();
+            ~Unlocked() { PyEval_RestoreThread(thread); }
+        };
+        moe_status s;
+        {
+            Unlocked u;
+            s = call();
+        }
+        return PyLong_FromLong(s);
+    }
 };
 
 // [G] matrices [N][K] with or without the leading G; several need offsets.
@@ -196,8 +212,10 @@ PyObject* balance_loss(PyObject*, PyObject* const* args, Py_ssize_t n) {
     void* ws = c.workspace(10, &bytes);
     if (!c.ok) return nullptr;
     if (!Args::fits_int({T, E, k})) return PyLong_FromLong(MOE_ERR_UNSUPPORTED);
-    return c.status(moe_balance_loss(logits, ids, mask, (int32_t)T, (int32_t)E, (int32_t)k, coef, loss, counts,
-                                     mean, tokens, ws, bytes, c.stream));
+    return c.status([&] {
+        return moe_balance_loss(logits, ids, mask, (int32_t)T, (int32_t)E, (int32_t)k, coef, loss, counts,
+                                mean, tokens, ws, bytes, c.stream);
+    });
 }
 
 // (dev, stream, logits, ids, w, dw, mask, renormalize, dloss, coef, counts, tokens, dlogits)
@@ -225,8 +243,10 @@ PyObject* route_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
     float* dlogits = const_cast<float*>(c.floats(12, "dlogits", {T, E}));
     if (!c.ok || renormalize < 0) return nullptr;
     if (!Args::fits_int({T, E, k})) return PyLong_FromLong(MOE_ERR_UNSUPPORTED);
-    return c.status(moe_route_backward(logits, ids, w, dw, mask, (int32_t)T, (int32_t)E, (int32_t)k, renormalize,
-                                       dloss, coef, counts, tokens, dlogits, c.stream));
+    return c.status([&] {
+        return moe_route_backward(logits, ids, w, dw, mask, (int32_t)T, (int32_t)E, (int32_t)k, renormalize,
+                                  dloss, coef, counts, tokens, dlogits, c.stream);
+    });
 }
 
 // (dev, stream, codes, scales, weight codes, weight scales, offsets, output, ws)
@@ -253,9 +273,11 @@ PyObject* product(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (!Args::fits_int({G, M, N, K})) return PyLong_FromLong(MOE_ERR_UNSUPPORTED);
     const at::ScalarType type = c.tensor(7, "output")->scalar_type();
     const int32_t out_type = type == at::kFloat ? MOE_OUT_F32 : type == at::kHalf ? MOE_OUT_F16 : MOE_OUT_BF16;
-    return c.status((INPUT ? moe_gemm_fp8_dgrad : moe_gemm_fp8)(a, as, w, wsc, offsets, (int32_t)G, (int32_t)M,
-                                                                (int32_t)N, (int32_t)K, out, out_type, ws, bytes,
-                                                                c.stream));
+    return c.status([&] {
+        return (INPUT ? moe_gemm_fp8_dgrad : moe_gemm_fp8)(a, as, w, wsc, offsets, (int32_t)G, (int32_t)M,
+                                                            (int32_t)N, (int32_t)K, out, out_type, ws, bytes,
+                                                            c.stream);
+    });
 }
 
 // (dev, stream, x, codes, scales): x gives the sizes; the buffers may have any shape, hold
@@ -272,8 +294,10 @@ PyObject* quantize_act(PyObject*, PyObject* const* args, Py_ssize_t n) {
     void* s = const_cast<void*>(c.reachable(4, "scales"));
     if (!c.ok) return nullptr;
     if (!Args::fits_int({cols})) return PyLong_FromLong(MOE_ERR_UNSUPPORTED);
-    return c.status(moe_quantize_act_fp8(static_cast<const uint16_t*>(x), M, (int32_t)cols,
-                                         static_cast<uint8_t*>(q), static_cast<float*>(s), c.stream));
+    return c.status([&] {
+        return moe_quantize_act_fp8(static_cast<const uint16_t*>(x), M, (int32_t)cols,
+                                    static_cast<uint8_t*>(q), static_cast<float*>(s), c.stream);
+    });
 }
 
 // (dev, stream, x, offsets, codes, scales)
@@ -293,9 +317,11 @@ PyObject* quantize_tokens(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const uint8_t* q = c.e4m3(4, "codes", {cols, R});
     const float* s = c.floats(5, "scales", {R / 128, cols});
     if (!c.ok) return nullptr;
-    return c.status(moe_quantize_fp8_tokens(static_cast<const uint16_t*>(x), offsets, (int32_t)G, (int32_t)M,
-                                            (int32_t)cols, const_cast<uint8_t*>(q), const_cast<float*>(s),
-                                            c.stream));
+    return c.status([&] {
+        return moe_quantize_fp8_tokens(static_cast<const uint16_t*>(x), offsets, (int32_t)G, (int32_t)M,
+                                       (int32_t)cols, const_cast<uint8_t*>(q), const_cast<float*>(s),
+                                       c.stream);
+    });
 }
 
 // (dev, stream, dy codes, dy scales, x codes, x scales, offsets, M, dw, accumulate, ws)
@@ -317,8 +343,10 @@ PyObject* wgrad(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int accumulate = PyObject_IsTrue(args[9]);
     void* ws = c.workspace(10, &bytes);
     if (!c.ok || accumulate < 0) return nullptr;
-    return c.status(moe_gemm_fp8_wgrad(dy, dys, x, xs, offsets, (int32_t)G, (int32_t)M, (int32_t)N, (int32_t)K, dw,
-                                       accumulate, ws, bytes, c.stream));
+    return c.status([&] {
+        return moe_gemm_fp8_wgrad(dy, dys, x, xs, offsets, (int32_t)G, (int32_t)M, (int32_t)N, (int32_t)K, dw,
+                                  accumulate, ws, bytes, c.stream);
+    });
 }
 
 // No C++ exception leaves an entry (a tensor without plain storage throws in its

@@ -3,6 +3,7 @@ binding does around a call."""
 import pytest
 import torch
 
+import binding_stub
 import train_ref as ref
 
 pytestmark = pytest.mark.gpu
@@ -38,3 +39,23 @@ def test_row_quantiser_on_larger_buffers_of_another_shape():
     M.quantize_act_fp8(x.to(DEV).view(torch.int16), gq, gs)
     assert torch.equal(gq[:1280].view(torch.uint8).view(5, 256).cpu(), q) and bool((gq[1280:] == 9).all())
     assert torch.equal(gs.view(-1)[:10].view(5, 2).cpu(), s) and bool((gs.view(-1)[10:] == 9.0).all())
+
+
+def test_every_call_lets_other_threads_run(tmp_path):
+    """A launch waits while the stream's queue is full; the interpreter lock held meanwhile
+    would stop the Python callback that could empty it."""
+    got = binding_stub.run(str(tmp_path), """
+z = lambda *s, t=torch.uint8: torch.zeros(s, dtype=t, device="cuda")
+f, i, b = torch.float32, torch.int32, torch.bfloat16
+logits, ids, w, ws = z(8, 16, t=f), z(8, 2, t=i), z(8, 2, t=f), z(256)
+one, n, counts = z(1, t=f), z(1, t=i), z(16, t=i)
+call("balance_loss", 0, 0, logits, ids, None, 0.1, one, counts, z(16, t=f), n, ws)
+call("route_backward", 0, 0, logits, ids, w, w, None, True, one, 0.1, counts, n, z(8, 16, t=f))
+a, s, m, ms = z(8, 128), z(8, 1, t=f), z(128, 128), z(1, 1, t=f)
+call("gemm_fp8", 0, 0, a, s, m, ms, None, z(8, 128, t=b), ws)
+call("gemm_fp8_dgrad", 0, 0, a, s, m, ms, None, z(8, 128, t=b), ws)
+call("quantize_act_fp8", 0, 0, z(8, 128, t=b), a, s)
+call("quantize_fp8_tokens", 0, 0, z(8, 128, t=b), None, m, z(1, 128, t=f))
+call("gemm_fp8_wgrad", 0, 0, m, z(1, 128, t=f), m, z(1, 128, t=f), None, 8, z(128, 128, t=f), False, ws)
+""")
+    assert got == {e.removeprefix("moe_"): 0 for e in binding_stub.ENTRIES}

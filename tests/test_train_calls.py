@@ -5,6 +5,8 @@ import ctypes
 import pytest
 import torch
 
+import binding_stub
+
 P = ctypes.c_void_p
 OKP = 1 << 20          # an aligned address; nothing is launched without a device
 
@@ -64,3 +66,10 @@ def test_row_quantiser_refuses_memory_that_the_device_does_not_reach(M):
     assert M._lib.moe_device_address(x.data_ptr()) is None
     with pytest.raises(ValueError, match="reaches"):
         M.quantize_act_fp8(x, q, s, stream=0)
+
+
+def test_a_call_lets_other_threads_run(tmp_path):
+    got = binding_stub.run(str(tmp_path), """
+call("quantize_act_fp8", 0, 0, torch.zeros((0, 128), dtype=torch.bfloat16), None, None)
+""")
+    assert got == {"quantize_act_fp8": 0}

@@ -99,11 +99,18 @@ struct Args {
     const float* floats(int i, const char* name, std::initializer_list<int64_t> sizes) {
         return static_cast<const float*>(data(i, name, sizes, f32, "float32"));
     }
-    float* floats_n(int i, const char* name, int64_t n) {
-        return const_cast<float*>(static_cast<const float*>(data(i, name, {}, f32, "float32", n)));
+    const float* floats_n(int i, const char* name, int64_t n) {
+        return static_cast<const float*>(data(i, name, {}, f32, "float32", n));
     }
-    int32_t* ints_n(int i, const char* name, int64_t n) {
-        return const_cast<int32_t*>(static_cast<const int32_t*>(data(i, name, {}, i32, "int32", n)));
+    const int32_t* ints_n(int i, const char* name, int64_t n) {
+        return static_cast<const int32_t*>(data(i, name, {}, i32, "int32", n));
+    }
+    // An output: `p` as the checks above gave it for tensor i, with storage of its own (a
+    // lazily cloned tensor still shares its source's).
+    template <typename T>
+    T* written(int i, const T* p) {
+        if (!ok || p == nullptr) return nullptr;
+        return static_cast<T*>(THPVariable_Unpack(a[i]).mutable_data_ptr());
     }
     const uint8_t* e4m3(int i, const char* name, std::initializer_list<int64_t> sizes) {
         return static_cast<const uint8_t*>(data(i, name, sizes, codes, "uint8 or float8_e4m3fn"));
@@ -141,17 +148,22 @@ struct Args {
         refuse(name, *t, want.c_str());
     }
     // The address of a contiguous tensor that the current device reaches: its own memory,
-    // pinned host memory, another device's with peer access; NULL for an empty one.
-    const void* reachable(int i, const char* name) {
-        if (none(i)) return nullptr;
+    // pinned host memory, another device's with peer access.
+    const void* reachable(int i, const char* name) { return reach(i, name, false); }
+    void* reachable_output(int i, const char* name) { return const_cast<void*>(reach(i, name, true)); }
+    const void* reach(int i, const char* name, bool write) {
         const at::Tensor* t = tensor(i, name);
-        if (t == nullptr || t->numel() == 0) return nullptr;
-        if (t->is_cuda() && t->get_device() == dev) return buffer(i, name);
-        const void* p = t->is_contiguous() ? moe_device_address(t->const_data_ptr()) : nullptr;
+        if (t == nullptr) return nullptr;
+        if (t->is_cuda() && t->get_device() == dev) {
+            const void* p = buffer(i, name);
+            return write ? written(i, p) : p;
+        }
+        const void* p = nullptr;
+        if (t->is_contiguous()) p = moe_device_address(write ? t->mutable_data_ptr() : t->const_data_ptr());
         if (p == nullptr) refuse(name, *t, "a buffer that the device reaches");
         return p;
     }
-    void* workspace(int i, size_t* bytes) { return const_cast<void*>(buffer(i, "workspace", bytes)); }
+    void* workspace(int i, size_t* bytes) { return written(i, buffer(i, "workspace", bytes)); }
     static bool fits_int(std::initializer_list<int64_t> v) {
         for (int64_t x : v)
             if (x < 0 || x > INT32_MAX) return false;
@@ -205,10 +217,10 @@ PyObject* balance_loss(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const uint8_t* mask =
         c.none(4) ? nullptr : static_cast<const uint8_t*>(c.data(4, "mask", {}, Args::flags, "uint8 or bool", T));
     const float coef = c.real(5);
-    float* loss = c.floats_n(6, "loss", 1);
-    int32_t* counts = c.ints_n(7, "counts", E);
-    float* mean = c.floats_n(8, "prob_mean", E);
-    int32_t* tokens = c.ints_n(9, "tokens", 1);
+    float* loss = c.written(6, c.floats_n(6, "loss", 1));
+    int32_t* counts = c.written(7, c.ints_n(7, "counts", E));
+    float* mean = c.written(8, c.floats_n(8, "prob_mean", E));
+    int32_t* tokens = c.written(9, c.ints_n(9, "tokens", 1));
     void* ws = c.workspace(10, &bytes);
     if (!c.ok) return nullptr;
     if (!Args::fits_int({T, E, k})) return PyLong_FromLong(MOE_ERR_UNSUPPORTED);
@@ -240,7 +252,7 @@ PyObject* route_backward(PyObject*, PyObject* const* args, Py_ssize_t n) {
         tokens = c.ints_n(11, "tokens", 1);
     }
     const float coef = c.real(9);
-    float* dlogits = const_cast<float*>(c.floats(12, "dlogits", {T, E}));
+    float* dlogits = c.written(12, c.floats(12, "dlogits", {T, E}));
     if (!c.ok || renormalize < 0) return nullptr;
     if (!Args::fits_int({T, E, k})) return PyLong_FromLong(MOE_ERR_UNSUPPORTED);
     return c.status([&] {
@@ -266,8 +278,8 @@ PyObject* product(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const float* wsc = grouped ? c.floats(5, "weight scales", {G, N / 128, K / 128})
                                : c.floats(5, "weight scales", {N / 128, K / 128});
     const int32_t* offsets = c.none(6) ? nullptr : c.ints_n(6, "offsets", G + 1);
-    void* out = const_cast<void*>(
-        c.data(7, "output", {M, out_cols}, Args::output, "bfloat16, uint16, float16 or float32"));
+    void* out = c.written(
+        7, c.data(7, "output", {M, out_cols}, Args::output, "bfloat16, uint16, float16 or float32"));
     void* ws = c.workspace(8, &bytes);
     if (!c.ok) return nullptr;
     if (!Args::fits_int({G, M, N, K})) return PyLong_FromLong(MOE_ERR_UNSUPPORTED);
@@ -289,9 +301,13 @@ PyObject* quantize_act(PyObject*, PyObject* const* args, Py_ssize_t n) {
     c.room(2, "x", Args::halves, "bfloat16, uint16 or int16", M * cols);
     c.room(3, "codes", Args::bytes, "uint8, int8 or float8_e4m3fn", M * cols);
     c.room(4, "scales", Args::f32, "float32", M * (cols / 128));
-    const void* x = c.reachable(2, "x");
-    void* q = const_cast<void*>(c.reachable(3, "codes"));
-    void* s = const_cast<void*>(c.reachable(4, "scales"));
+    const void* x = nullptr;
+    void *q = nullptr, *s = nullptr;
+    if (M * cols > 0) {  // else nothing is asked of the buffers
+        x = c.reachable(2, "x");
+        q = c.reachable_output(3, "codes");
+        s = c.reachable_output(4, "scales");
+    }
     if (!c.ok) return nullptr;
     if (!Args::fits_int({cols})) return PyLong_FromLong(MOE_ERR_UNSUPPORTED);
     return c.status([&] {
@@ -314,13 +330,12 @@ PyObject* quantize_tokens(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const int64_t R = moe_fp8_token_rows((int32_t)M, (int32_t)G);
     const void* x = c.data(2, "x", {M, cols}, Args::bf16, "bfloat16 or uint16");
     const int32_t* offsets = c.none(3) ? nullptr : c.ints_n(3, "offsets", G + 1);
-    const uint8_t* q = c.e4m3(4, "codes", {cols, R});
-    const float* s = c.floats(5, "scales", {R / 128, cols});
+    uint8_t* q = c.written(4, c.e4m3(4, "codes", {cols, R}));
+    float* s = c.written(5, c.floats(5, "scales", {R / 128, cols}));
     if (!c.ok) return nullptr;
     return c.status([&] {
         return moe_quantize_fp8_tokens(static_cast<const uint16_t*>(x), offsets, (int32_t)G, (int32_t)M,
-                                       (int32_t)cols, const_cast<uint8_t*>(q), const_cast<float*>(s),
-                                       c.stream);
+                                       (int32_t)cols, q, s, c.stream);
     });
 }
 
@@ -339,7 +354,7 @@ PyObject* wgrad(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const uint8_t* x = c.e4m3(4, "x codes", {K, R});
     const float* xs = c.floats(5, "x scales", {R / 128, K});
     const int32_t* offsets = c.none(6) ? nullptr : c.ints_n(6, "offsets", G + 1);
-    float* dw = c.floats_n(8, "dw", G * N * K);
+    float* dw = c.written(8, c.floats_n(8, "dw", G * N * K));
     const int accumulate = PyObject_IsTrue(args[9]);
     void* ws = c.workspace(10, &bytes);
     if (!c.ok || accumulate < 0) return nullptr;

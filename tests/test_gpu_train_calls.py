@@ -59,3 +59,41 @@ call("quantize_fp8_tokens", 0, 0, z(8, 128, t=b), None, m, z(1, 128, t=f))
 call("gemm_fp8_wgrad", 0, 0, m, z(1, 128, t=f), m, z(1, 128, t=f), None, 8, z(128, 128, t=f), False, ws)
 """)
     assert got == {e.removeprefix("moe_"): 0 for e in binding_stub.ENTRIES}
+
+
+def _calls():
+    """{entry: (function, its outputs by name)}: each with small inputs."""
+    f, i, b = torch.float32, torch.int32, torch.bfloat16
+    z = lambda *s, t=torch.uint8: torch.full(s, 1, dtype=t, device=DEV)  # noqa: E731
+    ws = z(256)
+    logits, ids, w, one, n, counts = z(8, 16, t=f), z(8, 2, t=i), z(8, 2, t=f), z(1, t=f), z(1, t=i), z(16, t=i)
+    a, s, m, ms, x, t = z(8, 128), z(8, 1, t=f), z(128, 128), z(1, 1, t=f), z(8, 128, t=b), z(1, 128, t=f)
+    return {
+        "balance_loss": (lambda loss, counts, mean, tokens, ws: M.balance_loss(
+            logits, ids, None, 0.1, loss, counts, mean, tokens, ws),
+            {"loss": (1, f), "counts": (16, i), "mean": (16, f), "tokens": (1, i), "ws": (256, torch.uint8)}),
+        "route_backward": (lambda dlogits: M.route_backward(
+            logits, ids, w, w, None, True, one, 0.1, counts, n, dlogits), {"dlogits": ((8, 16), f)}),
+        "gemm_fp8": (lambda y, ws: M.gemm_fp8(a, s, m, ms, None, y, ws),
+                     {"y": ((8, 128), b), "ws": (256, torch.uint8)}),
+        "gemm_fp8_dgrad": (lambda y: M.gemm_fp8_dgrad(a, s, m, ms, None, y, ws), {"y": ((8, 128), f)}),
+        "quantize_act_fp8": (lambda q, s: M.quantize_act_fp8(x, q, s), {"q": ((8, 128), torch.uint8), "s": ((8, 1), f)}),
+        "quantize_fp8_tokens": (lambda q, s: M.quantize_fp8_tokens(x, None, q, s),
+                                {"q": ((128, 128), torch.uint8), "s": ((1, 128), f)}),
+        "gemm_fp8_wgrad": (lambda dw: M.gemm_fp8_wgrad(m, t, m, t, None, 8, dw, True, ws), {"dw": ((128, 128), f)}),
+    }
+
+
+@pytest.mark.parametrize("entry", ["balance_loss", "route_backward", "gemm_fp8", "gemm_fp8_dgrad", "quantize_act_fp8",
+                                   "quantize_fp8_tokens", "gemm_fp8_wgrad"])
+def test_outputs_that_are_lazily_cloned_get_storage_of_their_own(entry):
+    """What a lazy clone shares with its source until it is written stays as it was."""
+    call, outputs = _calls()[entry]
+    plain = {n: torch.full(s if isinstance(s, tuple) else (s,), 5, dtype=t, device=DEV) for n, (s, t) in outputs.items()}
+    source = {n: t.clone() for n, t in plain.items()}
+    cloned = {n: torch._lazy_clone(t) for n, t in source.items()}
+    call(**plain)
+    call(**cloned)
+    for n, t in cloned.items():
+        assert bool((source[n] == 5).all()), f"{n}: the source was written"
+        assert torch.equal(t, plain[n]), n

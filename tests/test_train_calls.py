@@ -58,6 +58,7 @@ def test_row_quantiser_takes_empty_tensors_of_any_device(M):
     for x in (torch.zeros((0, 256), dtype=torch.bfloat16), torch.zeros((0, 256), dtype=torch.int16)):
         assert M._native.quantize_act_fp8(0, 0, x, q, s) == M.OK
         assert M._native.quantize_act_fp8(-1, 0, x, None, None) == M.OK
+        assert M._native.quantize_act_fp8(-1, 0, x, torch.zeros(9, dtype=torch.uint8), torch.zeros(9)) == M.OK
         M.quantize_act_fp8(x, q, s, stream=0)
 
 

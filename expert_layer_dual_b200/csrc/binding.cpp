@@ -41,7 +41,13 @@ struct Args {
             ok = false;
             return nullptr;
         }
-        return &THPVariable_Unpack(a[i]);
+        const at::Tensor& t = THPVariable_Unpack(a[i]);
+        if (t.is_neg() || t._is_zerotensor()) {  // their memory does not hold their values
+            PyErr_Format(PyExc_ValueError, "%s: a negated view or a zero without memory; resolve it first", name);
+            ok = false;
+            return nullptr;
+        }
+        return &t;
     }
 
     int64_t integer(int i) {

@@ -74,3 +74,23 @@ def test_a_call_lets_other_threads_run(tmp_path):
 call("quantize_act_fp8", 0, 0, torch.zeros((0, 128), dtype=torch.bfloat16), None, None)
 """)
     assert got == {"quantize_act_fp8": 0}
+
+
+@pytest.mark.parametrize("make", [lambda *s: torch._neg_view(torch.ones(s)),
+                                  lambda *s: torch._efficientzerotensor(s)], ids=["negated", "zero"])
+def test_tensors_whose_memory_does_not_hold_their_values_are_refused(M, make):
+    """The imaginary part of a conjugate is such a negated view; a mask of such zeros would
+    come without an address, as if there were no mask."""
+    n, z = M._native, torch.zeros
+    ids, i = z((4, 2), dtype=torch.int32), z(8, dtype=torch.int32)
+    assert torch.ones((1, 1), dtype=torch.complex64).conj().imag.is_neg()
+    with pytest.raises(ValueError, match="logits: a negated view or a zero"):
+        n.balance_loss(0, 0, make(4, 8), ids, None, 0.1, z(1), i, z(8), z(1), z(256))
+    with pytest.raises(ValueError, match="logits: a negated view or a zero"):
+        n.route_backward(0, 0, make(4, 8), ids, None, None, None, True, z(1), 0.1, i, i, z(4, 8))
+    with pytest.raises(ValueError, match="x: a negated view or a zero"):
+        n.quantize_act_fp8(0, 0, make(4, 128), z(4, 128, dtype=torch.uint8), z(4, 1))
+    with pytest.raises(ValueError, match="x: a negated view or a zero"):
+        n.quantize_fp8_tokens(0, 0, make(4, 128), None, z(128, 128), z(1, 128))
+    with pytest.raises(ValueError, match="dw: a negated view or a zero"):
+        n.gemm_fp8_wgrad(0, 0, i, i, i, i, None, 4, make(128, 128), False, z(256))

@@ -1,5 +1,5 @@
 """Builds the sm_100a shared library libmoe_b200.so in-tree with nvcc, and the
-native Python binding _moe_binding.so with g++.
+native Python binding _moe_binding.<interpreter>.torch-<version>.so with g++.
 
     python -m expert_layer_dual_b200.build [--force]
 
@@ -14,18 +14,25 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_b200.so")
-BINDING = os.path.join(HERE, "_moe_binding.so")
 SOURCES = ["api.cu", "routing.cu", "router.cu", "gemm_bf16.cu", "gemm_bf16_wide.cu", "gemm_bf16_2sm.cu", "gemm_fp8.cu", "gemm_mx.cu", "gemm_f8t.cu", "gemm_fp8_block.cu", "gemm_fp8_few.cu",
            "ep.cu", "allreduce_norm.cu", "noalloc.cu", "balance.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "--expt-relaxed-constexpr", "-I", INCLUDE]
+
+
+def binding_path() -> str:
+    """The native binding for this interpreter and this torch: it is compiled against both,
+    so its name says which, and another's is not found."""
+    import torch
+    return os.path.join(HERE, f"_moe_binding.{sysconfig.get_config_var('SOABI')}.torch-{torch.__version__}.so")
 
 
 def nvcc() -> str:
@@ -80,16 +87,13 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """The native argument marshalling (csrc/binding.cpp): a CPython module against
     this interpreter and its torch, linked to the library next to it."""
-    import sysconfig
     import torch
     src = os.path.join(CSRC, "binding.cpp")
-    stamp = os.path.join(BUILD, "binding.stamp")
-    made_with = f"{sys.version} torch {torch.__version__}"
-    same = os.path.exists(stamp) and open(stamp).read() == made_with
+    out = binding_path()
     newest = max(_mtime(src), _mtime(os.path.join(INCLUDE, "moe.h")))
-    if force or not same or _mtime(BINDING) < newest:
+    if force or _mtime(out) < newest:
         t = os.path.dirname(torch.__file__)
-        tmp = BINDING + f".tmp{os.getpid()}"
+        tmp = out + f".tmp{os.getpid()}"
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
                "-I", os.path.join(t, "include"),
@@ -99,12 +103,10 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
-        os.replace(tmp, BINDING)
-        with open(stamp, "w") as f:
-            f.write(made_with)
+        os.replace(tmp, out)
         if verbose:
-            print("built", BINDING)
-    return BINDING
+            print("built", out)
+    return out
 
 
 if __name__ == "__main__":

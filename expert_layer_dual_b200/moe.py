@@ -10,6 +10,8 @@ streams.
 
 Loading fails loudly: importing this module raises ``ImportError`` when the
 shared library has not been built (``python -m expert_layer_dual_b200.build``).
+The native binding belongs to one interpreter and torch version; without the one
+for these, the training entry points raise ``ImportError`` and the rest works.
 """
 from __future__ import annotations
 
@@ -20,6 +22,7 @@ from typing import Optional
 
 import torch
 
+from .build import binding_path
 from .configs import MoEConfig
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -31,13 +34,26 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 
+class _NoBinding:
+    """In the place of the native binding: every entry raises why there is none."""
+
+    def __init__(self, why: str):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError(f"{self._why}: build it with `python -m expert_layer_dual_b200.build`")
+
+
 def _load_native():
-    path = os.path.join(_HERE, "_moe_binding.so")
+    path = binding_path()
     if not os.path.exists(path):
-        raise ImportError(f"{path} is missing: build it with `python -m expert_layer_dual_b200.build`")
+        return _NoBinding(f"{path}, the binding for this interpreter and torch, is missing")
     spec = importlib.util.spec_from_file_location("_moe_binding", path)
     module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    try:
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        return _NoBinding(f"{path} does not load ({e})")
     return module
 
 
@@ -350,9 +366,29 @@ def quantize_act_fp8(x, q, scale, stream=None):
     codes in q (a byte each) and rows * cols / 128 scales in scale (f32), which may have any
     shape and hold more.  The tensors may lie in any memory that the current device reaches,
     pinned host memory among it."""
+    if isinstance(_native, _NoBinding):
+        return _quantize_act_fp8_ctypes(x, q, scale, stream)
     dev = _current_device() if torch.cuda.is_initialized() else -1
     _check(_native.quantize_act_fp8(dev, _stream(stream, None if dev < 0 else dev), x, q, scale),
            "moe_quantize_act_fp8")
+
+
+def _quantize_act_fp8_ctypes(x, q, scale, stream):
+    """The call without the native binding, with its checks."""
+    rows, cols = x.shape
+    n = rows * cols
+    buffers = (("x", x, (torch.bfloat16, torch.uint16, torch.int16), n),
+               ("codes", q, (torch.uint8, torch.int8, torch.float8_e4m3fn), n),
+               ("scales", scale, (torch.float32,), rows * (cols // 128)))
+    for name, t, types, need in buffers:
+        if need and (t.dtype not in types or t.numel() < need or not t.is_contiguous() or t.is_neg()):
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}; expected {need} elements or more of "
+                             f"{', '.join(str(d) for d in types)}, contiguous")
+    for name, t, _, need in buffers:
+        if need and not _lib.moe_device_address(t.data_ptr()):
+            raise ValueError(f"{name}: on {t.device}; expected memory that the current CUDA device reaches")
+    _check(_lib.moe_quantize_act_fp8(*(_p(x), rows, cols, _p(q), _p(scale)) if n else (None, rows, cols, None, None),
+                                     _stream(stream)), "moe_quantize_act_fp8")
 
 
 def quantize_weights_mxfp8(W, q, scale, stream=None):

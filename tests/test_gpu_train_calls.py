@@ -97,3 +97,17 @@ def test_outputs_that_are_lazily_cloned_get_storage_of_their_own(entry):
     for n, t in cloned.items():
         assert bool((source[n] == 5).all()), f"{n}: the source was written"
         assert torch.equal(t, plain[n]), n
+
+
+def test_row_quantiser_without_the_binding(monkeypatch):
+    """The same call, the same kernel, through ctypes."""
+    x = torch.randn((37, 384), generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    want = ref.quantise_rows(x)
+    monkeypatch.setattr(M, "_native", M._NoBinding("none"))
+    for place in (lambda t: t.to(DEV), lambda t: t.pin_memory()):
+        q, s = place(torch.zeros((37, 384), dtype=torch.uint8)), place(torch.zeros((37, 3)))
+        M.quantize_act_fp8(place(x), q, s)
+        torch.cuda.synchronize()
+        assert torch.equal(q.cpu(), want[0]) and torch.equal(s.cpu(), want[1])
+    with pytest.raises(ImportError):
+        M.gemm_fp8(q.to(DEV), s.to(DEV), q.to(DEV), s.to(DEV), None, q.to(DEV), q.to(DEV))

@@ -1,6 +1,9 @@
 """The training entry points' calls on the CPU: refusals, and what the native binding does
 around a call.  Nothing is launched: there is no device, or the call is refused before."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -94,3 +97,36 @@ def test_tensors_whose_memory_does_not_hold_their_values_are_refused(M, make):
         n.quantize_fp8_tokens(0, 0, make(4, 128), None, z(128, 128), z(1, 128))
     with pytest.raises(ValueError, match="dw: a negated view or a zero"):
         n.gemm_fp8_wgrad(0, 0, i, i, i, i, None, 4, make(128, 128), False, z(256))
+
+
+def test_another_torch_does_not_load_the_binding():
+    """The binding is compiled against one torch; under another the training calls raise, and
+    what does not need it works, the row quantiser with the same checks."""
+    code = """
+import torch
+torch.__version__ = "0.0.1"
+import expert_layer_dual_b200.moe as M
+z = torch.zeros
+bf, u8 = torch.bfloat16, torch.uint8
+assert M.workspace_bytes(M.moe_shape(4, 256, 8, 2, 128, 0, 0, 1)) > 0 and M.fp8_token_rows(5) == 128
+try:
+    M._native.gemm_fp8(0, 0, *[z(1)] * 7)
+except ImportError as e:
+    assert "torch-0.0.1" in str(e) and "expert_layer_dual_b200.build" in str(e), e
+else:
+    raise AssertionError("loaded")
+M.quantize_act_fp8(z((0, 256), dtype=bf), z((0, 256), dtype=u8), z((0, 2)), stream=0)
+M.quantize_act_fp8(z((0, 256), dtype=bf), None, None, stream=0)
+x, q, s = z((4, 256), dtype=bf), z((4, 256), dtype=u8), z((4, 2))
+for bad, name in (((x.half(), q, s), "x"), ((x, q[:3], s), "codes"), ((x, q, s.double()), "scales"), ((x, q, s), "x")):
+    try:
+        M.quantize_act_fp8(*bad, stream=0)
+    except ValueError as e:
+        assert str(e).startswith(name), e
+    else:
+        raise AssertionError(name)
+print("fine")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]

@@ -27,8 +27,12 @@
 // us, bound by the few warps its registers leave.  Few tokens are bound by the
 // launches: 3.7 and 3.3 us for 64.
 //
-// Sums are FP32 within a row and over a lane's rows, FP64 over the blocks; no
-// atomic on a float, so the results do not depend on scheduling.
+// Sums are FP32 within a row, over at most 64 rows of a lane and over a block's warps, FP64
+// over the blocks; what more rows of a lane would round away is kept beside their sums, so
+// the error does not grow with T.  No atomic on a float, so the results do not depend on
+// scheduling.
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -41,7 +45,15 @@ constexpr int kGroup = 4 * kLanes;       // columns of a row read at once
 constexpr int kWarps = 8;                // warps per block
 constexpr int kOneWarps = 32;            // warps of the one-block kernel
 constexpr int kRowWarps = 16;            // warps of the two-pass form's blocks
+constexpr int kTurns = 64;               // rows that a lane adds up in FP32
 constexpr int kFinishBlocks = 8;         // of k_balance_finish: 32 experts each
+
+// The loss's first pass: one block that finishes the result, two passes, or two passes over
+// so many tokens that a lane has more than kTurns rows (from 606209 tokens on).  The third
+// form against the second: 620000 tokens of 256 experts 104.4 and 102.2 us, of 8 experts 74.6
+// and 74.7, 2000000 of 64 226 and 227; with its additions in the second's place as well,
+// 131072 tokens of 256 took 29.0 us, so 27.6.
+enum Rows { kOneBlock, kTwoPasses, kManyRows };
 
 // NV: groups of 64 columns (E <= 64 NV); value 4i + c of lane l is column 64i + 4l + c.
 // VEC: E % 4 == 0, so the rows start on 16 bytes.
@@ -117,25 +129,59 @@ __device__ __forceinline__ float exp_row(float* v) {
     return s > 0.0f ? 1.0f / s : (s == 0.0f ? 0.0f : s);  // NaN stays NaN
 }
 
+// Adds a warp's sums, of its two rows together, to those in shared memory: hi, and lo of
+// what rounds away (first: there are none yet, lo unused where nothing follows); a lane
+// always has the same columns.
+template <int N>
+__device__ __forceinline__ void add_sums(float* hi, float* lo, float* acc, int l, int r, bool first) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        for (int o = kLanes; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    }
+    if (r == 0) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            float* const h = hi + i * kGroup + l * 4;
+            if (first) {
+                *reinterpret_cast<float4*>(h) = make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = h[j], b = acc[4 * i + j], s = a + b, d = s - a;
+                lo[i * kGroup + l * 4 + j] += (a - (s - d)) + (b - d);
+                h[j] = s;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+}
+
 // ---------------------------------------------------------------------------
 // Loss, first pass: a warp takes two tokens at a time and keeps the sums of its
 // tokens' probabilities in registers (a lane always holds the same columns);
 // the assignments are counted in shared memory (integers).  The block's sums go
 // to its row of the partials.  ONE: a single block, which finishes the result
-// itself (few tokens: one launch).
+// itself (few tokens: one launch).  MANY: after kTurns rows of a lane the warp's sums are
+// added to those in shared memory, each with its rounding error (Knuth's two-sum).
 // ---------------------------------------------------------------------------
-template <int NV, bool VEC, bool ONE, int WARPS>
+template <int NV, bool VEC, Rows FORM, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32)
     k_balance_rows(const float* __restrict__ logits, const int32_t* __restrict__ ids,
                    const uint8_t* __restrict__ mask, int T, int E, int k, BalancePartials part,
                    BalanceOut out) {
     constexpr int N = 4 * NV;
+    constexpr bool ONE = FORM == kOneBlock, MANY = FORM == kManyRows;
     __shared__ __align__(16) float s_psum[WARPS][kGroup * NV];
+    __shared__ __align__(16) float s_low[MANY ? WARPS : 1][MANY ? kGroup * NV : 1];  // rounded away of s_psum
     __shared__ int s_cnt[256], s_tokens, s_bad;
     __shared__ double s_term[8];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int l = lane % kLanes, r = lane / kLanes;
     for (int e = tid; e < 256; e += WARPS * 32) s_cnt[e] = 0;
+    if constexpr (MANY)
+        for (int i = tid; i < WARPS * kGroup * NV; i += WARPS * 32) s_low[0][i] = 0.0f;
     if (tid == 0) s_tokens = s_bad = 0;
     __syncthreads();
     pdl_trigger();
@@ -145,37 +191,35 @@ __global__ void __launch_bounds__(WARPS * 32)
 #pragma unroll
     for (int i = 0; i < N; ++i) acc[i] = 0.0f;
     int tokens = 0, bad = 0;
+    bool first = true;
     const int64_t step = (int64_t)gridDim.x * WARPS * kRows;
-    for (int64_t t0 = ((int64_t)blockIdx.x * WARPS + warp) * kRows; t0 < T; t0 += step) {
-        const int64_t t = t0 + r;
-        const bool on = t < T && (mask == nullptr || mask[t] != 0);
-        float v[N];
-        if (on) {
-            load_row<NV, VEC>(logits + t * E, E, l, v);
-            if (l < k) {
-                const int id = ids[t * k + l];
-                if (id >= 0 && id < E) atomicAdd(&s_cnt[id], 1);
-                else bad = 1;
+    int64_t t0 = ((int64_t)blockIdx.x * WARPS + warp) * kRows;
+    do {
+        const int64_t stop = MANY ? min((int64_t)T, t0 + kTurns * step) : T;
+        for (; t0 < stop; t0 += step) {
+            const int64_t t = t0 + r;
+            const bool on = t < T && (mask == nullptr || mask[t] != 0);
+            float v[N];
+            if (on) {
+                load_row<NV, VEC>(logits + t * E, E, l, v);
+                if (l < k) {
+                    const int id = ids[t * k + l];
+                    if (id >= 0 && id < E) atomicAdd(&s_cnt[id], 1);
+                    else bad = 1;
+                }
+                tokens += l == 0;
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] = -INFINITY;
             }
-            tokens += l == 0;
-        } else {
+            const float inv = exp_row<N>(v);
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] = -INFINITY;
+            for (int i = 0; i < N; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
         }
-        const float inv = exp_row<N>(v);
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = fmaf(v[i], inv, acc[i]);
-    }
-    // the warp's two rows, then the block's warps
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        for (int o = kLanes; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
-    }
-    if (r == 0)
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            *reinterpret_cast<float4*>(&s_psum[warp][i * kGroup + l * 4]) =
-                make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+        // the warp's two rows, then the block's warps
+        add_sums<N>(s_psum[warp], s_low[MANY ? warp : 0], acc, l, r, first);
+        first = false;
+    } while (MANY && t0 < T);
     tokens = __reduce_add_sync(0xffffffffu, tokens);
     if (bad) s_bad = 1;
     if (lane == 0 && tokens) atomicAdd(&s_tokens, tokens);
@@ -183,10 +227,13 @@ __global__ void __launch_bounds__(WARPS * 32)
 
     if (!ONE) {
         for (int e = tid; e < E; e += WARPS * 32) {
-            float s = 0.0f;
+            std::conditional_t<MANY, double, float> s = 0;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) s += s_psum[w][e];
-            part.psum[(int64_t)blockIdx.x * E + e] = s;
+            for (int w = 0; w < WARPS; ++w) {
+                s += s_psum[w][e];
+                if constexpr (MANY) s += s_low[w][e];
+            }
+            part.psum[(int64_t)blockIdx.x * E + e] = (float)s;
             part.cnt[(int64_t)blockIdx.x * E + e] = s_cnt[e];
         }
         if (tid == 0) {
@@ -444,10 +491,11 @@ struct LaunchRows {
     template <int NV, bool VEC>
     cudaError_t operator()() const {
         if (blocks == 1)
-            return launch_pdl(k_balance_rows<NV, VEC, true, kOneWarps>, dim3(1), dim3(kOneWarps * 32), 0, s,
+            return launch_pdl(k_balance_rows<NV, VEC, kOneBlock, kOneWarps>, dim3(1), dim3(kOneWarps * 32), 0, s,
                               logits, ids, mask, T, E, k, part, out);
-        return launch_pdl(k_balance_rows<NV, VEC, false, kRowWarps>, dim3(blocks), dim3(kRowWarps * 32), 0, s,
-                          logits, ids, mask, T, E, k, part, out);
+        const bool many = T > (int64_t)kTurns * blocks * kRowWarps * kRows;
+        return launch_pdl(many ? k_balance_rows<NV, VEC, kManyRows, kRowWarps> : k_balance_rows<NV, VEC, kTwoPasses, kRowWarps>,
+                          dim3(blocks), dim3(kRowWarps * 32), 0, s, logits, ids, mask, T, E, k, part, out);
     }
 };
 

@@ -604,29 +604,27 @@ __device__ __forceinline__ void quant_row(const uint16_t* __restrict__ src, int 
     }
 }
 
-// Rows as they are: a warp per 256 LOADS columns of a row, its 16-byte loads (LOADS per
-// lane) in flight together; the codes by GroupQuotient, the same codes as quant_row's.
-// The bytes bound it (2 read and 1 written per value), its instructions close behind:
-// with a chain of exchanges and a scale per load 8192 x 6144 took 30.0 us, so 26.9.
-// (A warp per row left 64 rows on eight SMs: 18 us at 6144 columns.)
+// Rows as they are, which are groups of 128 one after another, whatever the rows' length: a
+// warp per 256 LOADS values, its 16-byte loads (LOADS per lane) in flight together; the
+// codes by GroupQuotient, the same codes as quant_row's.  The bytes bound it (2 read and 1
+// written per value), its instructions close behind: 8192 x 6144 25.2 us, with a chain of
+// exchanges and a scale per load some 3 us more.  (A warp per row left 64 rows on eight SMs:
+// 18 us at 6144 columns; a warp per 1024 columns of a row left most of its lanes without
+// values in short rows: 1000000 x 128 293 us, so 60.)
 template <int LOADS>
 __global__ void __launch_bounds__(256, 6)
-    k_quant_act(const uint16_t* __restrict__ x, int64_t rows, int cols, uint8_t* __restrict__ q,
-                float* __restrict__ scale) {
+    k_quant_act(const uint16_t* __restrict__ x, int64_t n, uint8_t* __restrict__ q, float* __restrict__ scale) {
     pdl_trigger();
     pdl_wait();
-    const int64_t wid = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
-    const int nch = (cols + 256 * LOADS - 1) / (256 * LOADS);
-    const int64_t r = wid / nch;
-    if (r >= rows) return;
     const int lane = threadIdx.x & 31;
-    const int c0 = (int)(wid - r * nch) * (256 * LOADS) + lane * 8;
-    const uint16_t* src = x + r * cols + c0;
+    const int64_t first = ((blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5) * (256 * LOADS);
+    if (first >= n) return;
+    const int64_t e0 = first + lane * 8;
     uint4 u[LOADS];
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
         u[i] = make_uint4(0, 0, 0, 0);
-        if (c0 + i * 256 < cols) u[i] = __ldg(reinterpret_cast<const uint4*>(src + i * 256));
+        if (e0 + i * 256 < n) u[i] = __ldg(reinterpret_cast<const uint4*>(x + e0 + i * 256));
     }
     // the maxima of two groups (load i and i + 1) in a word through the exchanges
     uint32_t top[(LOADS + 1) / 2];
@@ -647,18 +645,17 @@ __global__ void __launch_bounds__(256, 6)
     const uint32_t pair = LOADS == 4 && (mine & 2) ? top[(LOADS - 1) / 2] : top[0];
     const GroupQuotient own(block_scale(__uint_as_float((mine & 1) ? pair & 0xFFFF0000u : pair << 16)));
     {
-        const int c = c0 + mine * 256;
-        if ((lane & 15) < LOADS && c < cols) scale[r * (cols / 128) + c / 128] = own.s;
+        const int64_t e = e0 + mine * 256;
+        if ((lane & 15) < LOADS && e < n) scale[e / 128] = own.s;
     }
 #pragma unroll
     for (int i = 0; i < LOADS; ++i) {
         const GroupQuotient g(__shfl_sync(0xffffffffu, own.s, (lane & 16) | i),
                               __shfl_sync(0xffffffffu, own.r, (lane & 16) | i));
-        const int c = c0 + i * 256;
-        if (c < cols)
-            *reinterpret_cast<uint2*>(q + r * cols + c) =
-                make_uint2(g.codes4(bf16x2_widen(u[i].x), bf16x2_widen(u[i].y)),
-                           g.codes4(bf16x2_widen(u[i].z), bf16x2_widen(u[i].w)));
+        const int64_t e = e0 + i * 256;
+        if (e < n)
+            *reinterpret_cast<uint2*>(q + e) = make_uint2(g.codes4(bf16x2_widen(u[i].x), bf16x2_widen(u[i].y)),
+                                                          g.codes4(bf16x2_widen(u[i].z), bf16x2_widen(u[i].w)));
     }
 }
 
@@ -754,17 +751,17 @@ cudaError_t launch_quant_act_fp8_scatter(const uint16_t* x, const int32_t* inv, 
 cudaError_t launch_quant_act_fp8(const uint16_t* x, int64_t rows, int cols, uint8_t* q,
                                  float* scale, cudaStream_t s) {
     if (rows == 0) return cudaSuccess;
-    // Long chunks for many rows, short ones where warps are few.  Measured with 1, 2 and 4
-    // loads: 1 x 2048 1.4, 1.5, 1.9 us; 64 x 6144 1.7, 1.7, 2.2; 512 x 4096 2.7, 3.0, 3.9;
-    // 3001 x 1408 (half a wave of warps with four loads) 4.5, 3.7, 4.3; 2048 x 4096 (a
-    // wave) 7.3, 5.9, 6.0; 4096 x 4096 (two) 14.4, 12.3, 10.8; 8192 x 6144 40.3, 32.5,
-    // 26.9 (5.6 TB/s).
-    const int64_t wave = (int64_t)current_device_info().num_sms * 48, chunks = rows * cols / 1024;
+    // Long chunks for many values, short ones where warps are few.  Measured with 1, 2 and 4
+    // loads: 1 x 2048 1.2, 1.3, 1.7 us; 64 x 6144 1.7, 1.7, 2.0; 512 x 4096 2.3, 2.9, 3.9;
+    // 3001 x 1408 (half a wave of warps with four loads) 4.1, 3.8, 4.7; 2048 x 4096 (a
+    // wave) 7.3, 6.2, 6.4; 4096 x 4096 (two) 12.8, 10.7, 10.1; 8192 x 6144 34.9, 27.9,
+    // 25.2 (6.0 TB/s); 1000000 x 128 86, 68, 60.
+    const int64_t n = rows * cols, wave = (int64_t)current_device_info().num_sms * 48, chunks = n / 1024;
     const int loads = chunks >= wave ? 4 : chunks >= wave / 2 ? 2 : 1;
-    const int64_t warps = rows * ((cols + 256 * loads - 1) / (256 * loads));
+    const int64_t warps = (n + 256 * loads - 1) / (256 * loads);
+    if ((warps + 7) / 8 >= ((int64_t)1 << 31)) return cudaErrorInvalidValue;
     const auto kernel = loads == 4 ? k_quant_act<4> : loads == 2 ? k_quant_act<2> : k_quant_act<1>;
-    const cudaError_t e = launch_pdl(kernel, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, x, rows, cols, q,
-                                     scale);
+    const cudaError_t e = launch_pdl(kernel, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, s, x, n, q, scale);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -111,3 +111,14 @@ def test_row_quantiser_without_the_binding(monkeypatch):
         assert torch.equal(q.cpu(), want[0]) and torch.equal(s.cpu(), want[1])
     with pytest.raises(ImportError):
         M.gemm_fp8(q.to(DEV), s.to(DEV), q.to(DEV), s.to(DEV), None, q.to(DEV), q.to(DEV))
+
+
+@pytest.mark.parametrize("shape", [(1, 128), (3, 128), (4097, 128), (60001, 128), (30001, 384), (12001, 640), (7001, 1152)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_row_quantiser_on_short_rows(shape):
+    """Groups of neighbouring rows share a warp; their number need not be even."""
+    x = (torch.randn(shape, generator=torch.Generator().manual_seed(shape[0])) * 3).to(torch.bfloat16)
+    want = ref.quantise_rows(x)
+    q, s = torch.full(shape, 9, dtype=torch.uint8, device=DEV), torch.full((shape[0], shape[1] // 128), 9.0, device=DEV)
+    M.quantize_act_fp8(x.to(DEV), q, s)
+    assert torch.equal(q.cpu(), want[0]) and torch.equal(s.cpu(), want[1])

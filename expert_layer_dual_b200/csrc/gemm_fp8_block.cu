@@ -564,8 +564,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             const CUtensorMap* map = is_a ? &tm_a : &tm_b;
             const uint32_t dst0 = sm.stages + (is_a ? 0 : A_BYTES);
             Ring<STAGES> st;
+            st.round = 1u;  // a producer waits for the round before; in the self-test for one that never ends
+            if (is_a && blockIdx.x + 1 == a.give_up) st.round = 0u;
             uint32_t issued = 0;
-            const uint32_t never = is_a && blockIdx.x + 1 == a.give_up;  // the self-test's wait
             bool ok = true;
             for (int i = work.first; ok && i < work.total; i += work.step) {
                 const PTile t = work.tile(a, sm.tt, i);
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     y = t.col0;
                 }
                 for (int kb = 0; kb < t.blocks; ++kb, st.next()) {
-                    if (!warp_wait_phase(sm.done(st.slot), st.round ^ 1u ^ never, a.timeout_ns, sm.abort_flag())) {
+                    if (!warp_wait_phase(sm.done(st.slot), st.round, a.timeout_ns, sm.abort_flag())) {
                         ok = false;
                         break;
                     }

@@ -241,8 +241,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         const bool is_w = warp == A_WARP;
         const CUtensorMap* map = is_w ? &tm_w : &tm_x;
         Ring<STAGES> st;
+        st.round = 1u;  // a producer waits for the round before; in the self-test for one that never ends
+        if (is_w && blockIdx.x + 1 == a.give_up) st.round = 0u;
         uint32_t issued = 0;
-        const uint32_t never = is_w && blockIdx.x + 1 == a.give_up;  // the self-test's wait
         bool ok = true;
         for (int i = first; ok && i < total; i += step) {
             const Tile t = decode_tile(sm.tt, a.G, n_tiles, i, FN);
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 if (INPUT) x = t.n * FM;
             }
             for (int kb = 0; kb < blocks; ++kb, st.next()) {
-                if (!warp_wait_phase(sm.done(st.slot), st.round ^ 1u ^ never, a.timeout_ns, sm.abort_flag())) {
+                if (!warp_wait_phase(sm.done(st.slot), st.round, a.timeout_ns, sm.abort_flag())) {
                     ok = false;
                     break;
                 }

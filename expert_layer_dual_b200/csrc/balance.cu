@@ -19,13 +19,13 @@
 // and a lane's values leave room for four blocks an SM, whose loads cover the
 // latency of memory.  Every logit is read once and every gradient written once, so
 // the bytes are the floor: 20 and 41 us for 131072 rows of 256 experts.  Measured
-// there: 27.6 us for the loss and 47.4 us for the gradient (4.8 and 5.7 TB/s;
-// 49.7 us with the top-k part).
+// there: 27.6 us for the loss and 47.0 us for the gradient (4.9 and 5.7 TB/s;
+// 49.5 us with the top-k part).
 // Other splits of a row took longer: a warp per row, with the accurate expf and
 // the top-k part by comparing every column with every id, 41 and 82 us, bound by
 // its instructions (210 and 496 a row); eight lanes with 32 values each 54 and 52
 // us, bound by the few warps its registers leave.  Few tokens are bound by the
-// launches: 3.7 and 3.3 us for 64.
+// launches: 3.6 and 3.2 us for 64.
 //
 // Sums are FP32 within a row, over at most 64 rows of a lane and over a block's warps, FP64
 // over the blocks; what more rows of a lane would round away is kept beside their sums, so
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(WARPS * 32)
 // all of them in flight together); the sums over the warps are in FP64 and in a fixed
 // order, as is the sum of the eight blocks' shares of the loss in the first block's
 // shared memory.  (With 64 blocks of four experts, the last of which added the shares
-// through global memory, the loss took 11.0 us for 16384 tokens, so 8.2.)
+// through global memory, the loss took 11.0 us for 16384 tokens, so 8.3.)
 __global__ void __cluster_dims__(kFinishBlocks, 1, 1) __launch_bounds__(1024)
     k_balance_finish(int E, int k, int nblocks, BalancePartials part, BalanceOut out) {
     constexpr int PER = (kBalanceMaxBlocks + 31) / 32;
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kWarps * 32, backward_blocks(NV))
         const int n = *a.tokens;
         cb = n > 0 ? *a.dloss * a.coef / (float)n : 0.0f;
         // a quotient per thread, then each lane's columns (in FP64 and sixteen a thread, 4096
-        // tokens took 5.4 us, so 4.7)
+        // tokens took 5.4 us, so 4.6); of two rounded integers, so within 1.5 * 2^-23
         if (tid < kGroup * NV) {
             const int64_t kn = (int64_t)k * n;
             s_f1[tid] = tid < E && n > 0 ? (float)((int64_t)a.counts[tid] * E - kn) / (float)kn : 0.0f;
@@ -506,7 +506,7 @@ struct LaunchBackward {
     cudaError_t operator()() const {
         const int64_t want = ((int64_t)a.T + kWarps * kRows - 1) / (kWarps * kRows);
         // as many blocks as are resident together, with turns of one length: 16384 tokens
-        // of 256 experts 10.1 us, 131072 49.8 us; with six per SM 10.9 and 55.7 us
+        // of 256 experts 9.0 us, 131072 49.5 us; with six per SM some 0.8 and 6 us more
         const int64_t most = (int64_t)current_device_info().num_sms * backward_blocks(NV);
         const int64_t turns = (want + most - 1) / most;
         return launch_pdl(k_route_backward<NV, VEC>, dim3((unsigned)((want + turns - 1) / turns)),

@@ -35,7 +35,11 @@ constexpr uint64_t kDefaultTimeoutNs = 2000000000ull;  // 2 s
 // memory is visible (a no-op for a kernel launched without the attribute),
 // so every kernel calls it before its first read of data another kernel
 // produced; pdl_trigger() lets the next kernel be scheduled once every block
-// of this one has passed it.
+// of this one has passed it.  A kernel may trigger before its own wait: the
+// next one then starts while the one before is still running, touches no
+// global memory until its wait, and that ends only when this kernel has, all
+// of whose threads have waited for the one before.  What a kernel takes before
+// its wait (shared memory, TMEM) it takes after every block of those ahead has.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

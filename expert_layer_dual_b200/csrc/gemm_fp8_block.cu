@@ -117,7 +117,8 @@ struct Work {
             const int per = n_tiles * k_tiles;
             p.g = i / per;
             const int r = i - p.g * per;
-            // rows first (columns first, 8192 x 4096 x 6144 took 258 us, so 252)
+            // rows first (columns first, 8192 x 4096 x 6144 took 252 us, so 249, and 32 experts of
+            // 2048 x 1408 over 5003 rows 78.6, so 76.1)
             p.row0 = (r % k_tiles) * BM;
             p.nrows = BM;
             p.col0 = (r / k_tiles) * BN;
@@ -336,8 +337,9 @@ __device__ __forceinline__ void bulk_wait() {
 // shared memory the rows of 32 columns lie as the tensor map's 128-byte swizzle has
 // them: 16-byte piece p of row r in place p ^ r.  (Stored from registers, after turning
 // chunks among four lanes, 32 experts of 2048 x 1408 over 5003 rows, 369 MB of output,
-// took 84.0 us, so 78.5; without the L2 policy 80.  The bytes alone take 50 us as a
-// fill, 56 at the copy's rate.)  A lane has row l / 4 and of each
+// took 84.0 us, so 78.6, and 76.1 with rows first; without the L2 policy 1.5 us more.  The bytes
+// alone take 50 us as a fill, 56 at the copy's rate.  Added to the output, which reads them
+// too, 166 us: the loads stand in front of the staging.)  A lane has row l / 4 and of each
 // eight columns a pair; odd rows take the groups of eight in another order, so that
 // the stores of half a warp fall on distinct banks.
 __device__ __forceinline__ void send_tile(const Fp8ProductArgs& a, const CUtensorMap* map, uint32_t buf,
@@ -494,12 +496,12 @@ __device__ __forceinline__ void add_tiles(const Fp8ProductArgs& a, const Smem& s
 // commit, wait, TMEM loads, products, arrival, next issue.  Cycles per block of a
 // 128 x 256 tile: 815 in all, 720 without the MMAs, 613 without the promotion,
 // 520 with neither.  At large sizes the power limit levels what is left of the
-// difference: 8192 x 4096 x 6144 takes 177 us (2.33 PFLOP/s) at ~1.5 GHz, 143 us
+// difference: 8192 x 4096 x 6144 takes 177 to 181 us (2.3 PFLOP/s) at ~1.5 GHz, 143 us
 // without its promotion, and variants with 5% fewer cycles took the same time
-// at a lower clock.  The weight gradient (two products a value) takes 252 us,
-// 4096 x 6144 x 2048 rows of the input gradient 52 us, 32 groups of 8192 rows 280
-// us (their 805 MB of weights alone 123 us; the groups' last tiles pad 336
-// tiles of rows to 432).
+// at a lower clock.  The weight gradient (two products a value) takes 249 us (268 added
+// to the output), 4096 x 6144 x 2048 rows of the input gradient 49 us, 32 groups of 8192 rows
+// 267 us (their 805 MB of weights alone 122 us; the groups' last tiles pad 336 tiles of
+// rows to 432).
 //
 // Sixteen epilogue warps of 64 accumulators each fit without spills (480 cycles of
 // promotion with spilled registers, so 256).  On CTA pairs (M = 256, the operands'
@@ -870,8 +872,8 @@ cudaError_t launch_tiles(Fp8ProductArgs a, cudaStream_t s) {
 
     // Few tiles and a long sum: as many CTAs a tile as find room.  Measured, one CTA
     // against the split: weight gradients of 1024 x 1024 (32 tiles, four CTAs each) over
-    // 2048 rows 15.2 against 16.6 us, 4096 rows 24.7 against 19.4, 16384 rows 80.8
-    // against 35.6; products of 1024 rows by 2048 columns (64 tiles, two each) with K =
+    // 2048 rows 14.7 against 16.6 us, 4096 rows 24.7 against 18.3, 16384 rows 80.8
+    // against 33.0; products of 1024 rows by 2048 columns (64 tiles, two each) with K =
     // 4096 19.2 against 19.6 us, 6144 26.1 against 24.1, 8192 33.2 against 28.4.  (A
     // launch of its own for the last wave's tiles, split so, gained 2% at 64 blocks
     // and lost 4% at 32.)

@@ -15,11 +15,12 @@
 // or 8 CTAs; each leaves its FP32 tile in its shared memory, and every CTA adds a
 // share of the rows over the cluster, in rank order (deterministic).
 //
-// Measured: 1 x 6144 x 2048 5.9 us, 1 x 4096 x 6144 7.6 us (the 128 x 256 tiles 23.5),
-// 64 x 4096 x 6144 9.7 us, the input gradient 64 x 6144 x 2048 8.3 us, and 1 x 8192 x
-// 8192 14.6 us (67 MB, 4.6 TB/s).  At the small sizes the weights' bytes would
-// take 2 to 4 us: the rest is the launch, the first load's latency and the
-// cluster's exchange.
+// Measured with the weights from DRAM: 1 x 6144 x 2048 6.9 us, 1 x 4096 x 6144 9.1, 64 x 4096 x
+// 6144 11.3, the input gradient 64 x 6144 x 2048 9.3, and 1 x 8192 x 8192 14.7 us (67 MB, 4.6
+// TB/s); with the weights in L2 the first four 5.9, 7.6 (the 128 x 256 tiles 23.5), 9.7 and
+// 8.3.  At the small sizes the weights' bytes would take 2 to 4 us: the rest is the launch,
+// the first load's latency and the cluster's exchange.  Grouped: 32 experts of 4096 x 6144 with
+// two rows each 122 us, with 16 rows 126 (805 MB of weights, 6.6 and 6.4 TB/s).
 #include <atomic>
 #include <mutex>
 

@@ -1162,7 +1162,8 @@ moe_status moe_selftest_product_timeout(int32_t op, const uint8_t* a, const floa
                                         const float* b_scale, int32_t M, int32_t N, int32_t K, float* out,
                                         int32_t accumulate, int32_t block, int32_t limit_us, void* ws,
                                         size_t ws_bytes, void* stream) {
-    if (op < 0 || op > 2 || block < 0 || limit_us <= 0 || limit_us > 1000000) return MOE_ERR_INVALID_ARG;
+    // below 1 ms a block could end while copies into its shared memory are in flight
+    if (op < 0 || op > 2 || block < 0 || limit_us < 1000 || limit_us > 1000000) return MOE_ERR_INVALID_ARG;
     const GiveUp g{(uint64_t)limit_us * 1000ull, (uint32_t)block};
     if (op == 2)
         return run_wgrad(a, a_scale, b, b_scale, nullptr, 1, M, N, K, out, accumulate, ws, ws_bytes, stream, &g);

@@ -578,7 +578,7 @@ void* moe_device_address(const void* p);
 
 /* Self-test of the FP8 products' failure path: runs the product (op 0:
  * moe_gemm_fp8, 1: moe_gemm_fp8_dgrad, 2: moe_gemm_fp8_wgrad; one group, FP32
- * output) with waits bounded by limit_us (at most 1 s), the first load of its
+ * output) with waits bounded by limit_us (1 ms to 1 s), the first load of its
  * thread block `block` waiting for a signal that never comes.  Records
  * MOE_ERR_DEVICE_TIMEOUT in ws's status word; the output tiles of that block, and of
  * the blocks that share them, are left as they were, the others are written. */

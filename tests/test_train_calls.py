@@ -21,11 +21,11 @@ def M():
 
 
 @pytest.mark.parametrize("change,code", [
-    ({"op": 3}, 1), ({"op": -1}, 1), ({"block": -1}, 1), ({"limit": 0}, 1), ({"limit": 1000001}, 1), ({"N": 100}, 2),
+    ({"op": 3}, 1), ({"op": -1}, 1), ({"block": -1}, 1), ({"limit": 0}, 1), ({"limit": 999}, 1), ({"limit": 1000001}, 1), ({"N": 100}, 2),
     ({"a": None}, 1), ({"out": OKP + 4}, 1), ({"ws": None}, 1), ({"ws_bytes": 128}, 4), ({"op": 2, "M": 9000000}, 2)])
 def test_selftest_refusals(M, change, code):
     a = {"op": 0, "a": OKP, "a_s": OKP, "b": OKP, "b_s": OKP, "M": 5, "N": 256, "K": 128, "out": OKP, "block": 0,
-         "limit": 100, "ws": OKP, "ws_bytes": 256, **change}
+         "limit": 1000, "ws": OKP, "ws_bytes": 256, **change}
     assert M._lib.moe_selftest_product_timeout(
         a["op"], P(a["a"]), P(a["a_s"]), P(a["b"]), P(a["b_s"]), a["M"], a["N"], a["K"], P(a["out"]), 0, a["block"],
         a["limit"], P(a["ws"]), a["ws_bytes"], None) == code

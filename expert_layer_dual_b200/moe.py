@@ -41,6 +41,8 @@ class _NoBinding:
         self._why = why
 
     def __getattr__(self, name):
+        if name.startswith("__"):  # what introspection asks of any object
+            raise AttributeError(name)
         raise ImportError(f"{self._why}: build it with `python -m expert_layer_dual_b200.build`")
 
 

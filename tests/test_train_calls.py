@@ -109,6 +109,7 @@ import expert_layer_dual_b200.moe as M
 z = torch.zeros
 bf, u8 = torch.bfloat16, torch.uint8
 assert M.workspace_bytes(M.moe_shape(4, 256, 8, 2, 128, 0, 0, 1)) > 0 and M.fp8_token_rows(5) == 128
+assert not hasattr(M._native, "__wrapped__")  # as inspect and doctest ask
 try:
     M._native.gemm_fp8(0, 0, *[z(1)] * 7)
 except ImportError as e:

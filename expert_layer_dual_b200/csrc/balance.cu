@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(WARPS * 32)
     const int l = lane % kLanes, r = lane / kLanes;
     for (int e = tid; e < 256; e += WARPS * 32) s_cnt[e] = 0;
     if constexpr (MANY)
-        for (int i = tid; i < WARPS * kGroup * NV; i += WARPS * 32) s_low[0][i] = 0.0f;
+        for (int i = lane; i < kGroup * NV; i += 32) s_low[warp][i] = 0.0f;
     if (tid == 0) s_tokens = s_bad = 0;
     __syncthreads();
     pdl_trigger();

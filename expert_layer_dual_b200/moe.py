@@ -597,9 +597,21 @@ def selftest_product_timeout(op: int, a, a_s, b, b_s, M: int, out, accumulate, b
                              stream=None):
     """moe_selftest_product_timeout: the operands of gemm_fp8 (op 0), gemm_fp8_dgrad (1) or
     gemm_fp8_wgrad (2) for one group; out float32, [M, N], [M, K] or [N, K]."""
-    if out.dtype != torch.float32:
-        raise ValueError(f"out: {out.dtype}; expected float32")
     N, K = out.shape if op == 2 else b.shape
+    R = fp8_token_rows(M)
+    byte, f32 = (torch.uint8, torch.float8_e4m3fn), (torch.float32,)
+    if op == 2:
+        shapes = (N, R), (R // 128, N), (K, R), (R // 128, K), (N, K)
+    else:
+        i, o = (N, K) if op else (K, N)
+        shapes = (M, i), (M, i // 128), (N, K), (N // 128, K // 128), (M, o)
+    for name, t, shape, types in zip(("a", "a_s", "b", "b_s", "out"), (a, a_s, b, b_s, out), shapes,
+                                     (byte, f32, byte, f32, f32)):
+        if t.shape != shape or t.dtype not in types:
+            raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}; expected {shape} "
+                             f"{' or '.join(str(d).removeprefix('torch.') for d in types)}")
+    for t in (a, a_s, b, b_s, out, ws):
+        _launch_device(t)
     _check(_lib.moe_selftest_product_timeout(op, _p(a), _p(a_s), _p(b), _p(b_s), M, N, K, _p(out), int(accumulate),
                                              int(block), int(limit_us), _p(ws), ws.numel() * ws.element_size(),
                                              _stream(stream)), "moe_selftest_product_timeout")

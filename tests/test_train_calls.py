@@ -31,10 +31,20 @@ def test_selftest_refusals(M, change, code):
         a["limit"], P(a["ws"]), a["ws_bytes"], None) == code
 
 
-def test_selftest_takes_fp32_outputs_only(M):
-    z = torch.zeros((128, 128), dtype=torch.uint8)
-    with pytest.raises(ValueError, match="float32"):
-        M.selftest_product_timeout(0, z, z, z, z, 128, torch.zeros((128, 128), dtype=torch.bfloat16), False, 0, 100, z)
+@pytest.mark.parametrize("op,shapes", [(0, ((9, 384), (9, 3), (256, 384), (2, 3), (9, 256))),
+                                       (1, ((9, 256), (9, 2), (256, 384), (2, 3), (9, 384))),
+                                       (2, ((256, 128), (1, 256), (384, 128), (1, 384), (256, 384)))])
+def test_selftest_checks_its_tensors(M, op, shapes):
+    types = (torch.uint8, torch.float32, torch.uint8, torch.float32, torch.float32)
+    good = [torch.zeros(s, dtype=t) for s, t in zip(shapes, types)]
+    ws = torch.zeros(256, dtype=torch.uint8)
+    call = lambda t: M.selftest_product_timeout(op, *t[:4], 9, t[4], False, 0, 1000, ws, stream=0)  # noqa: E731
+    with pytest.raises(ValueError, match="current CUDA device"):
+        call(good)
+    for i, name in enumerate(("a", "a_s", "b", "b_s", "out")):
+        for bad in (good[i][:-1], good[i].to(torch.bfloat16)):
+            with pytest.raises(ValueError, match="expected"):
+                call([*good[:i], bad, *good[i + 1:]])
 
 
 @pytest.mark.parametrize("change,want", [
